@@ -337,6 +337,46 @@ int m2rnn_gate_rmsnorm_bwd(int64_t rows, int64_t D, int io_dtype, int param_dtyp
                            void* dy, void* dg_pre, void* dgamma, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/*
+ * The selective state-space scan: the recurrence's linear sibling in the same
+ * layout, for layers of both kinds in one model.  Per batch row b and head n, from
+ * the initial state H_0 (K x V):
+ *
+ *     d_t = softplus(logit_t + beta[n]),   f_t = exp(-alpha[n] d_t)   (m2rnn_gates' exp-softplus form)
+ *     H_t = f_t H_{t-1} + d_t k_t v_t^T
+ *     y_t = H_t^T q_t + w_r[n] (.) v_t
+ *
+ * (k, q, v are the layer's B, C and x; d its step size, alpha = -A its decay rate and
+ * w_r = D its skip weight.)  alpha >= 0 and finite inputs are preconditions, except that
+ * logit = -inf is defined: d_t = 0 and f_t = 1, the token leaves the state as it was (a
+ * padding or masked token; its gradients through d_t are 0).
+ *
+ * fp32 state: in_dtype F32 or BF16 is the type of k, v, q, y, dy, dk, dv, dq (bf16 results
+ * are rounded to nearest even once); logit, alpha, beta, w_r, the states and every other
+ * gradient are F32, and so are all sums.  The sizes, shared q/k heads, empty calls and
+ * other conventions are those at the top of this file.
+ *
+ * Workspace (device bytes, 16-byte aligned) of m2rnn_ssm_fwd (is_bwd = 0) or
+ * m2rnn_ssm_bwd (is_bwd = 1); 0 = none.
+ */
+size_t m2rnn_ssm_workspace_bytes(int is_bwd, int64_t B, int64_t T, int64_t n_heads,
+                                 int64_t qk_heads, int64_t K, int64_t V, int in_dtype);
+
+/*
+ * m2rnn_ssm_fwd -- the scan over T tokens from H0 (or zero).  A long prompt may be given
+ * in pieces, each starting from the piece before's HT.
+ *   k, q   [B, T, qk_heads, K]  in, in_dtype
+ *   v      [B, T, n_heads, V]   in, in_dtype
+ *   logit  [B, T, n_heads]      in;  alpha, beta [n_heads] in;  w_r [n_heads, V] in
+ *   H0     [B, n_heads, K, V]   in, or NULL for zero
+ *   y      [B, T, n_heads, V]   out, in_dtype
+ *   HT     [B, n_heads, K, V]   out, or NULL
+ */
+int m2rnn_ssm_fwd(int64_t B, int64_t T, int64_t n_heads, int64_t qk_heads, int64_t K, int64_t V,
+                  int in_dtype, const void* k, const void* v, const void* q, const void* logit,
+                  const void* alpha, const void* beta, const void* w_r, const void* H0, void* y,
+                  void* HT, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

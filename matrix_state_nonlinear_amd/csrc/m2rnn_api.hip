@@ -8,6 +8,7 @@
 #include "../../include/m2rnn.h"
 #include "m2rnn_internal.h"
 #include "m2rnn_newton_internal.h"
+#include "m2rnn_ssm_internal.h"
 
 using namespace m2rnn;
 
@@ -466,6 +467,45 @@ int m2rnn_gate_rmsnorm_bwd(int64_t rows, int64_t D, int io_dtype, int param_dtyp
   a.rows = rows; a.D = D; a.eps = eps; a.y = y; a.g_pre = g_pre; a.gamma = gamma;
   a.dout = dout; a.dy = dy; a.dg_pre = dg_pre; a.dgamma = dgamma; a.ws = workspace;
   return status_of(launch_gate_rmsnorm(a, io_dtype, param_dtype, true, st));
+}
+
+// ---- the state-space scan
+
+size_t m2rnn_ssm_workspace_bytes(int is_bwd, int64_t B, int64_t T, int64_t n_heads,
+                                 int64_t qk_heads, int64_t K, int64_t V, int in_dtype) {
+  if (!sizes_ok(B, T, n_heads, K, V) || !qk_heads_ok(n_heads, qk_heads) || is_bwd ||
+      !dtypes_ok(in_dtype, M2RNN_F32) || !sizes_supported(B, T, n_heads, K, V) ||
+      B * T * n_heads == 0)
+    return 0;
+  const SsmLayout L = ssm_fwd_layout(B, T, n_heads, K, V, in_dtype);
+  return align_up(L.total_floats * 4, 256);
+}
+
+int m2rnn_ssm_fwd(int64_t B, int64_t T, int64_t n_heads, int64_t qk_heads, int64_t K, int64_t V,
+                  int in_dtype, const void* k, const void* v, const void* q, const void* logit,
+                  const void* alpha, const void* beta, const void* w_r, const void* H0, void* y,
+                  void* HT, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!sizes_ok(B, T, n_heads, K, V) || !qk_heads_ok(n_heads, qk_heads) ||
+      !in_dtype_known(in_dtype))
+    return M2RNN_ERR_INVALID_ARG;
+  const bool empty = B * T * n_heads == 0;
+  if (!empty && (!k || !v || !q || !logit || !alpha || !beta || !w_r || !y))
+    return M2RNN_ERR_INVALID_ARG;
+  if (!dtypes_ok(in_dtype, M2RNN_F32) || !sizes_supported(B, T, n_heads, K, V))
+    return M2RNN_ERR_UNSUPPORTED;
+  const hipStream_t st = (hipStream_t)stream;
+  if (empty) return status_of(fill(HT, H0, B * n_heads * K * V, M2RNN_F32, st));
+  const SsmLayout L = ssm_fwd_layout(B, T, n_heads, K, V, in_dtype);
+  const size_t need = align_up(L.total_floats * 4, 256);
+  if (need && (!workspace || workspace_bytes < need)) return M2RNN_ERR_WORKSPACE;
+  if (need && !aligned16(workspace)) return M2RNN_ERR_INVALID_ARG;
+  SsmArgs a{};
+  a.k = k; a.v = v; a.q = q;
+  a.logit = (const float*)logit; a.alpha = (const float*)alpha; a.beta = (const float*)beta;
+  a.w_r = (const float*)w_r; a.H0 = (const float*)H0;
+  a.y = y; a.HT = (float*)HT; a.ws = (float*)workspace;
+  a.B = B; a.T = T; a.N = n_heads; a.NQ = qk_heads; a.K = K; a.V = V;
+  return status_of(launch_ssm_fwd(a, in_dtype, st));
 }
 
 }  // extern "C"

@@ -1,0 +1,104 @@
+// Host-side interface of the selective state-space scan (m2rnn_ssm_*.hip) for
+// the C ABI (m2rnn_api.hip), and the argument blocks of its kernels.
+#pragma once
+
+#include "m2rnn_internal.h"
+
+namespace m2rnn {
+
+// One pass of the decayed linear attention that the scan and its gradients
+// consist of (m2rnn_ssm_sweep.h): for a head, over the tokens p in walking order,
+//     out_p = rho_p (sum_{p' <= p} D_{pp'} g_{p'} (a_p . b_p') c_p' + R_p S^T a_p) [+ skip (.) c_p]
+// from the state S [DA, DC] carried in.
+struct SsmSweepArgs {
+  const void* a;        // [B, T, N / a_grp, DA]: head n reads head n / a_grp
+  const void* b;        // [B, T, N / b_grp, DA]
+  const void* c;        // [B, T, N / c_grp, DC]
+  const void* e;        // [B, T, N / e_grp, DC] or null: rowdot_p = e_p . (out_p / rho_p, no skip)
+  const float* logit;   // [B, T, N]
+  const float* alpha;   // [N]
+  const float* beta;    // [N]
+  const float* skip;    // [N, DC] or null
+  void* out;            // [B, T, N, DC], input type, or fp32 when out_f32
+  float* rowdot;        // [slabs, B, N, T] (e given)
+  float* colsum;        // [B, N, nseg, DA] or null: sum_p a_p (.) b_p
+  const float* state0;  // [B, N, nseg, *] segment starts (or [B, N, *] when nseg = 1), or null = 0
+  float* stateT;        // [B, N, *] or null: the state after the last token (nseg = 1 only)
+  const float* hend;    // base only: [B, N, nseg, *], the other state at each segment's end is
+                        // entry s + 1, and hend_last [B, N, *] for the last one
+  const float* hend_last;
+  float* base;          // [slabs, B, N, nseg] or null: <state0, hend> of every segment
+  int64_t B, T, N, nseg, seglen, slabs;
+  int a_grp, b_grp, c_grp, e_grp;
+  int DA, DC;
+  int a_stride, c_stride;  // element strides of a state along DA and DC
+  int rev;                 // walk from the last token to the first
+  int w_in, w_out;         // the write strength d_p multiplies the inputs (g) / the outputs (rho)
+  int out_f32;
+  int va, vb, vc, ve, vo;  // 16-byte (a, b, c) and 4-element (e, out) accesses allowed
+};
+
+// State that each segment of T adds to a zero start, and its decay.
+struct SsmContribArgs {
+  const void* b;        // [B, T, N / b_grp, DA]
+  const void* c;        // [B, T, N / c_grp, DC]
+  const float* logit;
+  const float* alpha;
+  const float* beta;
+  float* contrib;       // [B, N, nseg, DA, DC]
+  float* fseg;          // [B, N, nseg] decay over a segment, or null
+  int64_t B, T, N, nseg, seglen, slabs;
+  int b_grp, c_grp;
+  int DA, DC;
+  int rev, w_in;
+  int vb, vc;
+};
+
+// Whole-call arguments (device pointers checked by the ABI).
+struct SsmArgs {
+  const void* k;
+  const void* v;
+  const void* q;
+  const float* logit;
+  const float* alpha;
+  const float* beta;
+  const float* w_r;
+  const float* H0;      // may be null
+  void* y;              // forward
+  float* HT;            // forward, may be null
+  const void* dy;       // backward
+  const float* dHT;     // may be null
+  void* dk;
+  void* dv;
+  void* dq;
+  float* dlogit;
+  float* dw_r;
+  float* dalpha;
+  float* dbeta;
+  float* dH0;           // may be null
+  float* ws;
+  int64_t B, T, N, NQ, K, V;
+};
+
+// Workspace of a call: offsets in floats (64-float aligned) and the split of T
+// into nseg segments of seglen tokens.
+struct SsmLayout {
+  int64_t nseg, seglen;
+  size_t hseg, fseg;                       // [B, N, nseg, K, V], [B, N, nseg] (nseg > 1 or backward)
+  size_t gseg, hT, base, udot, zdot;       // backward
+  size_t colsum, gatepart, dqp, dkp;
+  size_t total_floats;
+};
+SsmLayout ssm_fwd_layout(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V, int in_dtype);
+hipError_t launch_ssm_fwd(const SsmArgs& a, int in_dtype, hipStream_t stream);
+
+// The sweep's instances, one input type per file (they compile in parallel).
+hipError_t launch_ssm_sweep_bf16(const SsmSweepArgs& a, hipStream_t stream);
+hipError_t launch_ssm_sweep_f32(const SsmSweepArgs& a, hipStream_t stream);
+hipError_t launch_ssm_sweep(const SsmSweepArgs& a, int in_dtype, hipStream_t stream);
+hipError_t launch_ssm_contrib(const SsmContribArgs& a, int in_dtype, hipStream_t stream);
+hipError_t launch_ssm_segscan(float* seg, const float* fseg, const float* first, float* last,
+                              int64_t units, int64_t nseg, int64_t KV, bool rev,
+                              hipStream_t stream);
+
+}  // namespace m2rnn

@@ -1,0 +1,821 @@
+// The selective state-space scan as a chunked sweep on the matrix cores.
+//
+// Per head, H_t = f_t H_{t-1} + d_t k_t v_t^T and y_t = H_t^T q_t.  Over a chunk of
+// L tokens that starts from the state S (c_p the sum of log2 f up to token p of
+// the chunk, all exponents <= 0):
+//     y_p  = sum_{p' <= p} 2^{c_p - c_p'} d_p' (q_p . k_p') v_p' + 2^{c_p} S^T q_p
+//     S   <- 2^{c_L} S + sum_p 2^{c_L - c_p} d_p k_p v_p^T
+// which is four matrix products a chunk instead of L dependent steps.  The three
+// gradients of the sequence tensors are the same sum with the tensors in other
+// places (R the state gradient, walked from the last token to the first):
+//     dq: a = dy, b = v,  c = k, forward,  state H^T
+//     dv: a = k,  b = q,  c = dy, reverse, state R,   d_p on the output
+//     dk: a = v,  b = dy, c = q,  reverse, state R^T, d_p on the output
+// so one kernel computes all four.
+//
+// A workgroup (4 waves) walks one segment of one head, the state in MFMA
+// accumulators throughout: wave w owns 16 NT columns of it, all DA rows.  All
+// products use the 16x16x32 bf16 MFMA (16 times the rate of the fp32 one); bf16
+// inputs are exact operands, and every fp32 operand (the decayed scores, the state,
+// the decayed inputs of the state update, and fp32 inputs) is split into bf16
+// terms whose sum is the fp32 value: three for what is summed into the state (24
+// bits, exact), two for the scores and the state's readout when the inputs and
+// outputs are bf16 (relative error 2^-17 against the output's 2^-9), three of them for
+// fp32 inputs.  Operands are taken so that an accumulator layout is the next
+// product's operand layout: the state's accumulators are the readout's operand without
+// a move, and an output lane holds four consecutive columns.
+#pragma once
+
+#include "m2rnn_device.h"
+#include "m2rnn_ssm_internal.h"
+
+namespace m2rnn {
+namespace ssm {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Tokens per chunk: 64 for bf16 inputs, 32 for fp32 ones (three bf16 planes each in LDS).
+template <typename InT>
+struct Cfg;
+template <>
+struct Cfg<uint16_t> {
+  static constexpr int L = 64, planes = 1, score_terms = 2, state_terms = 2, epc = 8;
+};
+template <>
+struct Cfg<float> {
+  static constexpr int L = 32, planes = 3, score_terms = 3, state_terms = 3, epc = 4;
+};
+
+__device__ __forceinline__ f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+// acc += (sum of a's terms) (sum of b's terms), leaving out the products below the
+// last term kept (2^-24 of the result).
+template <int PA, int PB>
+__device__ __forceinline__ f32x4 mfma_terms(const bf16x8 (&a)[PA], const bf16x8 (&b)[PB], f32x4 c) {
+#pragma unroll
+  for (int i = PA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = PB - 1; j >= 0; --j)
+      if (i + j <= 2) c = mfma_bf16(a[i], b[j], c);
+  return c;
+}
+
+__device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint32_t, x); }
+// (by value: a bit cast of a vector's element in place reads element 0)
+__device__ __forceinline__ float as_float(uint32_t u) { return __builtin_bit_cast(float, u); }
+__device__ __forceinline__ float hi_part(float x) {  // x truncated to bf16
+  return __builtin_bit_cast(float, bits(x) & 0xFFFF0000u);
+}
+// two values truncated to bf16, the first in the low half
+__device__ __forceinline__ uint32_t pack_trunc(float x0, float x1) {
+  return __builtin_amdgcn_perm(bits(x1), bits(x0), 0x07060302u);
+}
+// two values rounded to nearest even
+__device__ __forceinline__ uint32_t pack_rne(float x0, float x1) {
+  const bf16x2 p{(__bf16)x0, (__bf16)x1};
+  return __builtin_bit_cast(uint32_t, p);
+}
+// x0, x1 as P bf16 terms: truncation for all but the last of two, which is rounded;
+// three truncated terms hold all 24 bits.
+template <int P>
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t (&t)[P]) {
+  static_assert(P == 2 || P == 3, "");
+  t[0] = pack_trunc(x0, x1);
+  const float r0 = x0 - hi_part(x0), r1 = x1 - hi_part(x1);
+  if constexpr (P == 2) {
+    t[1] = pack_rne(r0, r1);
+  } else {
+    t[1] = pack_trunc(r0, r1);
+    t[2] = pack_trunc(r0 - hi_part(r0), r1 - hi_part(r1));
+  }
+}
+template <int P>
+__device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&f)[P]) {
+  uint32_t w[P][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t t[P];
+    split2<P>(x[2 * i], x[2 * i + 1], t);
+#pragma unroll
+    for (int p = 0; p < P; ++p) w[p][i] = t[p];
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+    f[p] = __builtin_bit_cast(bf16x8, u32x4{w[p][0], w[p][1], w[p][2], w[p][3]});
+}
+__device__ __forceinline__ float lo_half(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
+__device__ __forceinline__ float hi_half(uint32_t u) {
+  return __builtin_bit_cast(float, u & 0xFFFF0000u);
+}
+// sums of the terms of eight values (exact: largest first, 24 bits in all)
+template <int P>
+__device__ __forceinline__ void widen8(const bf16x8 (&f)[P], float (&x)[8]) {
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const u32x4 u = __builtin_bit_cast(u32x4, f[p]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = p ? x[2 * i] + lo_half(u[i]) : lo_half(u[i]);
+      x[2 * i + 1] = p ? x[2 * i + 1] + hi_half(u[i]) : hi_half(u[i]);
+    }
+  }
+}
+
+// ------------------------------------------------------------- LDS operands
+// Eight values of one row that are consecutive along it.
+__device__ __forceinline__ bf16x8 row8(const uint16_t* p) {
+  return __builtin_bit_cast(bf16x8, *(const u32x4*)p);
+}
+// Columns 4 g .. 4 g + 3 and 16 + 4 g .. of a 32-column block (p at the block's column
+// 4 g): the order in which two 16-row accumulator tiles hold their rows.
+__device__ __forceinline__ bf16x8 row4x2(const uint16_t* p) {
+  const u32x2 x = *(const u32x2*)p, y = *(const u32x2*)(p + 16);
+  return __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
+}
+// Eight consecutive rows of one column per lane: the transposing read gives lane l of a
+// 16-lane group column l of four rows whose 16 columns the group's lanes address
+// in pieces of four (lane s: row s / 4, columns 4 (s % 4)).  p: the group's first row at the
+// block's first column; stride in elements.
+__device__ __forceinline__ bf16x8 col8(const uint16_t* p, int stride, int m) {
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  const uint16_t* s = p + (m >> 2) * stride + (m & 3) * 4;
+  const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)s);
+  const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(s + 4 * stride));
+  const u32x2 xx = __builtin_bit_cast(u32x2, x), yy = __builtin_bit_cast(u32x2, y);
+  return __builtin_bit_cast(bf16x8, u32x4{xx[0], xx[1], yy[0], yy[1]});
+}
+
+// ------------------------------------------------------------- staging
+// A tile of L rows (tokens) x W columns: 16-byte pieces, N of them per thread, fetched
+// into registers while the chunk before is worked on and written to LDS after it.
+template <typename InT, int W>
+struct Tile {
+  static constexpr int L = Cfg<InT>::L, EPC = Cfg<InT>::epc, CPR = W / EPC,
+                       N = L * CPR / 256, STRIDE = W + 8, PLANE = L * STRIDE;
+  static_assert(L * CPR % 256 == 0, "");
+  u32x4 r[N];
+
+  // rows p < len come from token first + step p; columns >= D and rows >= len are zero
+  __device__ __forceinline__ void fetch(const InT* base, int64_t row_stride, int64_t first, int step,
+                                        int len, int D, bool vec) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int id = (int)threadIdx.x + 256 * i;
+      const int row = id / CPR, col = (id % CPR) * EPC;
+      u32x4 x{0, 0, 0, 0};
+      if (row < len && col < D) {
+        const InT* p = base + (first + (int64_t)step * row) * row_stride + col;
+        if (vec) {
+          x = *(const u32x4*)p;
+        } else {
+#pragma unroll
+          for (int j = 0; j < EPC; ++j) {
+            if (col + j < D) {
+              if constexpr (EPC == 8)
+                x[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+              else
+                x[j] = bits(p[j]);
+            }
+          }
+        }
+      }
+      r[i] = x;
+    }
+  }
+  __device__ __forceinline__ void put(uint16_t* lds) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int id = (int)threadIdx.x + 256 * i;
+      uint16_t* p = lds + (id / CPR) * STRIDE + (id % CPR) * EPC;
+      if constexpr (EPC == 8) {
+        *(u32x4*)p = r[i];
+      } else {
+        uint32_t t0[3], t1[3];
+        split2<3>(as_float(r[i][0]), as_float(r[i][1]), t0);
+        split2<3>(as_float(r[i][2]), as_float(r[i][3]), t1);
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) *(u32x2*)(p + pl * PLANE) = u32x2{t0[pl], t1[pl]};
+      }
+    }
+  }
+  // acc[j] += x[j] y[j] over this thread's pieces (its columns are the same in every piece)
+  static __device__ __forceinline__ void dot_cols(const Tile& x, const Tile& y, float (&acc)[EPC]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < EPC; ++j) {
+        if constexpr (EPC == 8) {
+          const uint32_t u = x.r[i][j / 2], w = y.r[i][j / 2];
+          acc[j] += (j & 1) ? hi_half(u) * hi_half(w) : lo_half(u) * lo_half(w);
+        } else {
+          acc[j] += as_float(x.r[i][j]) * as_float(y.r[i][j]);
+        }
+      }
+  }
+};
+
+// ------------------------------------------------------------- decays of a chunk
+// Per token p of the chunk, from the exact (double) prefix sums c_p: every power has an
+// exponent <= 0 and is rounded once.
+template <int L>
+struct Gates {
+  float R[L];      // 2^{c_p}: from the carried state to p
+  float W[L];      // 2^{c_end - c_p} g_p: from p to the state carried on
+  float eg[L];     // 2^{c_tile_end - c_p} g_p (tiles of 16 tokens)
+  float rr[L / 16 - 1][L];  // 2^{c_p - c_end(tile j)}, j below p's tile
+  float chi[L], clo[L];     // c_p in two parts, for the tiles on the diagonal
+  float g[L];      // input weight
+  float rho[L];    // output weight
+  float total;     // 2^{c_end}
+};
+
+__device__ __forceinline__ float pow2(double c) {
+  const double n = __builtin_rint(c);
+  return __builtin_ldexpf(__builtin_amdgcn_exp2f((float)(c - n)), (int)n);
+}
+__device__ __forceinline__ float softplus(float x) {
+  return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
+}
+// log2 f, held at -2048 or more: 2^-2048 is already zero in fp32, and the sums of a chunk
+// then keep their low bits.
+__device__ __forceinline__ double log2_decay(float alpha, float d) {
+  return fmax(-(double)alpha * (double)d * 1.4426950408889634, -2048.0);
+}
+__device__ __forceinline__ double shfl_d(double x, int lane) { return __shfl(x, lane); }
+
+// One wave: lane p has the logit of the chunk's token p (walking order) in x.  Going
+// forward the decay into p counts at p (inclusive sums); in reverse the decay between p
+// and p + 1 is p's own, so the sums are exclusive.
+template <int L>
+__device__ __forceinline__ void make_gates(Gates<L>& G, float x, float alpha, float beta, int len,
+                                           bool rev, bool w_in, bool w_out) {
+  const int lane = threadIdx.x & 63;
+  const float d = lane < len ? softplus(x + beta) : 0.0f;
+  const double l2 = lane < len ? log2_decay(alpha, d) : 0.0;
+  double inc = l2;
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) {
+    const double o = __shfl_up(inc, s);
+    if (lane >= s) inc += o;
+  }
+  const double total = shfl_d(inc, 63);
+  double prev = __shfl_up(inc, 1);
+  if (lane == 0) prev = 0.0;
+  const double c = rev ? prev : inc;
+  const double tile_end = shfl_d(c, lane | 15);
+  const float g = w_in ? d : 1.0f;
+  float rr[L / 16 - 1];
+#pragma unroll
+  for (int j = 0; j < L / 16 - 1; ++j) {
+    const double e = shfl_d(c, 16 * j + 15);
+    rr[j] = lane >= 16 * (j + 1) ? pow2(c - e) : 0.0f;
+  }
+  if (lane < L) {
+    G.R[lane] = pow2(c);
+    G.W[lane] = pow2(total - c) * g;
+    G.eg[lane] = pow2(tile_end - c) * g;
+#pragma unroll
+    for (int j = 0; j < L / 16 - 1; ++j) G.rr[j][lane] = rr[j];
+    const float hi = (float)c;
+    G.chi[lane] = hi;
+    G.clo[lane] = (float)(c - (double)hi);
+    G.g[lane] = g;
+    G.rho[lane] = w_out ? d : 1.0f;
+  }
+  if (lane == 0) G.total = pow2(total);
+}
+
+// ------------------------------------------------------------- the sweep
+template <typename InT, int AT, int NT>
+struct SweepShared {
+  using C = Cfg<InT>;
+  static constexpr int L = C::L;
+  using TA = Tile<InT, 32 * AT>;
+  using TC = Tile<InT, 64 * NT>;
+  static constexpr int PSTRIDE = L + 8;
+  alignas(16) uint16_t a[C::planes * TA::PLANE];
+  alignas(16) uint16_t b[C::planes * TA::PLANE];
+  alignas(16) uint16_t c[C::planes * TC::PLANE];
+  alignas(16) uint16_t p[C::score_terms][L * PSTRIDE];
+  alignas(16) Gates<L> g[2];
+  alignas(16) float red[4][L];
+};
+
+template <typename InT>
+__device__ __forceinline__ void store_cols4(void* out, int64_t i, f32x4 x, int left, bool vec,
+                                            bool f32) {
+  if (f32 || sizeof(InT) == 4) {
+    float* p = (float*)out + i;
+    if (vec) {
+      *(f32x4*)p = x;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r < left) p[r] = x[r];
+    }
+  } else {
+    uint16_t* p = (uint16_t*)out + i;
+    const u32x2 u{pack_rne(x[0], x[1]), pack_rne(x[2], x[3])};
+    if (vec) {
+      *(u32x2*)p = u;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r < left) p[r] = (uint16_t)(u[r / 2] >> (16 * (r & 1)));
+    }
+  }
+}
+template <typename InT>
+__device__ __forceinline__ f32x4 load_cols4(const InT* p, int left, bool vec) {
+  f32x4 x{0, 0, 0, 0};
+  if (vec) {
+    if constexpr (sizeof(InT) == 2) {
+      const u32x2 u = *(const u32x2*)p;
+      x = f32x4{lo_half(u[0]), hi_half(u[0]), lo_half(u[1]), hi_half(u[1])};
+    } else {
+      x = *(const f32x4*)p;
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (r < left) x[r] = load_in(p + r);
+  }
+  return x;
+}
+
+template <typename InT, int AT, int NT>
+__global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 1)
+    m2rnn_ssm_sweep_kernel(const SsmSweepArgs g) {
+  using C = Cfg<InT>;
+  using S = SweepShared<InT, AT, NT>;
+  using TA = typename S::TA;
+  using TC = typename S::TC;
+  constexpr int L = C::L, NI = L / 16, P = C::planes, PS = C::score_terms, PH = C::state_terms;
+  __shared__ S sh;
+
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, m = lane & 15, q4 = lane >> 4;
+  // workgroup id -> (b, segment, head, slab), slabs then heads fastest: the heads that
+  // share q and k, and the slabs of a head, run on one XCD and share its L2
+  int64_t u = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+  const int slab = (int)(u % g.slabs);
+  u /= g.slabs;
+  const int n = (int)(u % g.N);
+  u /= g.N;
+  const int64_t seg = u % g.nseg;
+  const int64_t bi = u / g.nseg;
+  const int64_t bn = bi * g.N + n;
+  const int c0 = slab * 64 * NT;           // first column of this workgroup
+  const bool rev = g.rev != 0;
+
+  const int64_t seg0 = seg * g.seglen;
+  const int64_t seg1 = seg0 + g.seglen < g.T ? seg0 + g.seglen : g.T;
+  const int nch = (int)((seg1 - seg0 + L - 1) / L);
+
+  const int64_t ah = g.N / g.a_grp, bh = g.N / g.b_grp, ch_ = g.N / g.c_grp;
+  const InT* pa = (const InT*)g.a + (bi * g.T * ah + n / g.a_grp) * g.DA;
+  const InT* pb = (const InT*)g.b + (bi * g.T * bh + n / g.b_grp) * g.DA;
+  const InT* pc = (const InT*)g.c + (bi * g.T * ch_ + n / g.c_grp) * g.DC + c0;
+  const int64_t sa = ah * g.DA, sb = bh * g.DA, sc = ch_ * g.DC;
+  const float* pl = g.logit + bi * g.T * g.N + n;
+  const float alpha = g.alpha[n], beta = g.beta[n];
+  const int dc = g.DC - c0;                // columns left from c0
+
+  // the chunk i in walking order: first token, walking step and length
+  auto chunk_at = [&](int i) { return seg0 + (int64_t)(rev ? nch - 1 - i : i) * L; };
+  auto chunk_len = [&](int64_t t0) { return (int)(seg1 - t0 < L ? seg1 - t0 : L); };
+  const int step = rev ? -1 : 1;
+  auto first_tok = [&](int64_t t0, int len) { return rev ? t0 + len - 1 : t0; };
+  auto logit_of = [&](int i) {
+    const int64_t t0 = chunk_at(i);
+    const int len = chunk_len(t0);
+    return lane < len ? pl[(first_tok(t0, len) + step * lane) * g.N] : 0.0f;
+  };
+
+  // scores above the diagonal stay zero: only tiles on and below it are ever written
+  for (int i = threadIdx.x; i < (int)(sizeof(sh.p) / 16); i += 256) ((u32x4*)sh.p)[i] = u32x4{0, 0, 0, 0};
+
+  // state: rows 16 at + 4 q4 + r, column 16 ct + m of this workgroup's columns
+  f32x4 st[2 * AT][NT];
+  {
+    const int64_t kv = (int64_t)g.DA * g.DC;
+    const float* s0 = g.state0 ? g.state0 + (bn * g.nseg + seg) * kv : nullptr;
+    const float* he = nullptr;
+    if (g.base)
+      he = seg + 1 < g.nseg ? g.hend + (bn * g.nseg + seg + 1) * kv : g.hend_last + bn * kv;
+    float dot = 0.0f;
+#pragma unroll
+    for (int at = 0; at < 2 * AT; ++at)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int ai = 16 * at + 4 * q4 + r, ci = c0 + 16 * (w * NT + nt) + m;
+          const bool ok = ai < g.DA && ci < g.DC;
+          const int64_t o = (int64_t)ai * g.a_stride + (int64_t)ci * g.c_stride;
+          const float x = (s0 && ok) ? s0[o] : 0.0f;
+          st[at][nt][r] = x;
+          if (he && ok) dot += x * he[o];
+        }
+    if (g.base) {
+#pragma unroll
+      for (int s = 1; s < 64; s *= 2) dot += __shfl_xor(dot, s);
+      if (lane == 0) sh.red[w][0] = dot;
+      __syncthreads();
+      if (threadIdx.x == 0)
+        g.base[((int64_t)slab * g.B * g.N + bn) * g.nseg + seg] =
+            (sh.red[0][0] + sh.red[1][0]) + (sh.red[2][0] + sh.red[3][0]);
+      __syncthreads();
+    }
+  }
+
+  TA fa, fb;
+  TC fc;
+  float csum[C::epc];
+#pragma unroll
+  for (int j = 0; j < C::epc; ++j) csum[j] = 0.0f;
+  const bool do_col = g.colsum != nullptr && slab == 0;
+
+  float xl = 0.0f;  // wave 3: the logits of the next chunk whose gates it makes
+  {
+    const int64_t t0 = chunk_at(0);
+    const int len = chunk_len(t0);
+    fa.fetch(pa, sa, first_tok(t0, len), step, len, g.DA, g.va);
+    fb.fetch(pb, sb, first_tok(t0, len), step, len, g.DA, g.vb);
+    fc.fetch(pc, sc, first_tok(t0, len), step, len, dc, g.vc);
+    if (w == 3) {
+      const float x = logit_of(0);
+      if (nch > 1) xl = logit_of(1);
+      make_gates<L>(sh.g[0], x, alpha, beta, len, rev, g.w_in, g.w_out);
+    }
+    fa.put(sh.a);
+    fb.put(sh.b);
+    fc.put(sh.c);
+    if (do_col) TA::dot_cols(fa, fb, csum);
+  }
+  __syncthreads();
+
+  for (int ch = 0; ch < nch; ++ch) {
+    const int64_t t0 = chunk_at(ch);
+    const int len = chunk_len(t0);
+    const Gates<L>& G = sh.g[ch & 1];
+    if (ch + 1 < nch) {
+      const int64_t t1 = chunk_at(ch + 1);
+      const int len1 = chunk_len(t1);
+      fa.fetch(pa, sa, first_tok(t1, len1), step, len1, g.DA, g.va);
+      fb.fetch(pb, sb, first_tok(t1, len1), step, len1, g.DA, g.vb);
+      fc.fetch(pc, sc, first_tok(t1, len1), step, len1, dc, g.vc);
+    }
+
+    // scores: tile (it, jt), jt <= it, of a b^T, decayed and split.  Waves 0..2 take every
+    // third tile; wave 3 the last one of ten and the next chunk's gates.
+    constexpr int TILES = NI * (NI + 1) / 2;
+#pragma unroll
+    for (int rd = 0; rd < (TILES > 9 ? 3 : (TILES + 2) / 3); ++rd) {
+      const int idx = w < 3 ? rd * 3 + w : (rd == 0 && TILES > 9 ? 9 : TILES);
+      if (idx < TILES) {
+        const int it = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0;
+        const int jt = idx - it * (it + 1) / 2;
+        f32x4 s{0, 0, 0, 0};
+        const uint16_t* ra = sh.a + (16 * it + m) * TA::STRIDE + 8 * q4;
+        const uint16_t* rb = sh.b + (16 * jt + m) * TA::STRIDE + 8 * q4;
+#pragma unroll
+        for (int t = 0; t < AT; ++t) {
+          bf16x8 xa[P], xb[P];
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            xa[p] = row8(ra + p * TA::PLANE + 32 * t);
+            xb[p] = row8(rb + p * TA::PLANE + 32 * t);
+          }
+          s = mfma_terms(xb, xa, s);
+        }
+        // lane: token i = 16 it + m, inputs j = 16 jt + 4 q4 + r
+        const int i = 16 * it + m, j0 = 16 * jt + 4 * q4;
+        if (it == jt) {
+          const f32x4 ch4 = *(const f32x4*)(G.chi + j0), cl4 = *(const f32x4*)(G.clo + j0),
+                      g4 = *(const f32x4*)(G.g + j0);
+          const float hi = G.chi[i], lo = G.clo[i];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float dec = __builtin_amdgcn_exp2f((hi - ch4[r]) + (lo - cl4[r])) * g4[r];
+            s[r] = j0 + r <= i ? s[r] * dec : 0.0f;
+          }
+        } else {
+          const f32x4 e4 = *(const f32x4*)(G.eg + j0);
+          const float ri = G.rr[jt][i];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[r] *= ri * e4[r];
+        }
+        uint32_t x0[PS], x1[PS];
+        split2<PS>(s[0], s[1], x0);
+        split2<PS>(s[2], s[3], x1);
+#pragma unroll
+        for (int p = 0; p < PS; ++p)
+          *(u32x2*)(sh.p[p] + i * S::PSTRIDE + j0) = u32x2{x0[p], x1[p]};
+      }
+    }
+    if (w == 3 && ch + 1 < nch) {
+      make_gates<L>(sh.g[(ch + 1) & 1], xl, alpha, beta, chunk_len(chunk_at(ch + 1)), rev, g.w_in,
+                    g.w_out);
+      if (ch + 2 < nch) xl = logit_of(ch + 2);
+    }
+
+    // readout of the carried state: lane holds out[i = 16 it + m][c = 4 q4 + r]
+    f32x4 acc[NI][NT];
+#pragma unroll
+    for (int it = 0; it < NI; ++it)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) acc[it][nt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int t = 0; t < AT; ++t) {
+      bf16x8 hs[NT][PH];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const f32x4 lo = st[2 * t][nt], hi = st[2 * t + 1][nt];
+        const float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        split8<PH>(x, hs[nt]);
+      }
+#pragma unroll
+      for (int it = 0; it < NI; ++it) {
+        bf16x8 xa[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          xa[p] = row4x2(sh.a + p * TA::PLANE + (16 * it + m) * TA::STRIDE + 32 * t + 4 * q4);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[it][nt] = mfma_terms(hs[nt], xa, acc[it][nt]);
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < NI; ++it) {
+      const float R = G.R[16 * it + m];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) acc[it][nt] *= R;
+    }
+    __syncthreads();  // the scores are in LDS
+
+    // the chunk's own inputs, and what they leave in the state
+    const float ftot = G.total;
+#pragma unroll
+    for (int at = 0; at < 2 * AT; ++at)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) st[at][nt] *= ftot;
+#pragma unroll
+    for (int jb = 0; jb < L / 32; ++jb) {
+      bf16x8 cw[NT][3];
+      const f32x4 w0 = *(const f32x4*)(G.W + 32 * jb + 8 * q4),
+                  w1 = *(const f32x4*)(G.W + 32 * jb + 8 * q4 + 4);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        bf16x8 xc[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          xc[p] = col8(sh.c + p * TC::PLANE + (32 * jb + 8 * q4) * TC::STRIDE + 16 * (w * NT + nt),
+                       TC::STRIDE, m);
+#pragma unroll
+        for (int it = 2 * jb; it < NI; ++it) {
+          bf16x8 xp[PS];
+#pragma unroll
+          for (int p = 0; p < PS; ++p)
+            xp[p] = row8(sh.p[p] + (16 * it + m) * S::PSTRIDE + 32 * jb + 8 * q4);
+          acc[it][nt] = mfma_terms(xc, xp, acc[it][nt]);
+        }
+        float x[8];
+        widen8<P>(xc, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= j < 4 ? w0[j & 3] : w1[j & 3];
+        split8<3>(x, cw[nt]);
+      }
+#pragma unroll
+      for (int at = 0; at < 2 * AT; ++at) {
+        bf16x8 xb[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          xb[p] = col8(sh.b + p * TA::PLANE + (32 * jb + 8 * q4) * TA::STRIDE + 16 * at, TA::STRIDE, m);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) st[at][nt] = mfma_terms(xb, cw[nt], st[at][nt]);
+      }
+    }
+
+    // output
+#pragma unroll
+    for (int it = 0; it < NI; ++it) {
+      const int i = 16 * it + m;
+      const bool ok = i < len;
+      const int64_t tok = first_tok(t0, len) + step * i;
+      float dot = 0.0f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int cc = 16 * (w * NT + nt) + 4 * q4;
+        f32x4 x = acc[it][nt];
+        const int left = dc - cc;
+        if (g.e && ok && left > 0) {
+          const InT* pe = (const InT*)g.e +
+                          ((bi * g.T + tok) * (g.N / g.e_grp) + n / g.e_grp) * g.DC + c0 + cc;
+          const f32x4 ev = load_cols4(pe, left, g.ve);
+          dot += (ev[0] * x[0] + ev[1] * x[1]) + (ev[2] * x[2] + ev[3] * x[3]);
+        }
+        x *= G.rho[i];
+        if (g.skip && left > 0) {
+          f32x4 cv{0, 0, 0, 0};
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            const u32x2 uu = *(const u32x2*)(sh.c + p * TC::PLANE + i * TC::STRIDE + cc);
+            cv += f32x4{lo_half(uu[0]), hi_half(uu[0]), lo_half(uu[1]), hi_half(uu[1])};
+          }
+          const float* ps = g.skip + (int64_t)n * g.DC + c0 + cc;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (r < left) x[r] += ps[r] * cv[r];
+        }
+        if (ok && left > 0)
+          store_cols4<InT>(g.out, ((bi * g.T + tok) * g.N + n) * g.DC + c0 + cc, x, left, g.vo,
+                           g.out_f32);
+      }
+      if (g.e) {
+        dot += __shfl_xor(dot, 16);
+        dot += __shfl_xor(dot, 32);
+        if (q4 == 0) sh.red[w][i] = dot;
+      }
+    }
+    __syncthreads();  // everybody is done with the tiles
+    if (g.e && threadIdx.x < L && (int)threadIdx.x < len) {
+      const int i = threadIdx.x;
+      g.rowdot[((int64_t)slab * g.B * g.N + bn) * g.T + first_tok(t0, len) + step * i] =
+          (sh.red[0][i] + sh.red[1][i]) + (sh.red[2][i] + sh.red[3][i]);
+    }
+    if (ch + 1 < nch) {
+      fa.put(sh.a);
+      fb.put(sh.b);
+      fc.put(sh.c);
+      if (do_col) TA::dot_cols(fa, fb, csum);
+      __syncthreads();
+    }
+  }
+
+  if (g.stateT) {
+    float* sT = g.stateT + bn * (int64_t)g.DA * g.DC;
+#pragma unroll
+    for (int at = 0; at < 2 * AT; ++at)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int ai = 16 * at + 4 * q4 + r, ci = c0 + 16 * (w * NT + nt) + m;
+          if (ai < g.DA && ci < g.DC)
+            sT[(int64_t)ai * g.a_stride + (int64_t)ci * g.c_stride] = st[at][nt][r];
+        }
+  }
+  if (do_col) {  // threads with the same columns: 256 / CPR of them, summed in order
+    __syncthreads();
+    float* red = (float*)sh.a;
+#pragma unroll
+    for (int j = 0; j < C::epc; ++j) red[threadIdx.x * C::epc + j] = csum[j];
+    __syncthreads();
+    for (int col = threadIdx.x; col < g.DA; col += 256) {
+      float sum = 0.0f;
+      for (int k = col / C::epc; k < 256; k += TA::CPR) sum += red[k * C::epc + col % C::epc];
+      g.colsum[(bn * g.nseg + seg) * g.DA + col] = sum;
+    }
+  }
+}
+
+// The state a segment adds to a zero start: the sweep's state update alone.
+template <typename InT, int AT, int NT>
+__global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 1)
+    m2rnn_ssm_contrib_kernel(const SsmContribArgs g) {
+  using C = Cfg<InT>;
+  using TB = Tile<InT, 32 * AT>;
+  using TC = Tile<InT, 64 * NT>;
+  constexpr int L = C::L, P = C::planes;
+  struct Sh {
+    alignas(16) uint16_t b[P * TB::PLANE];
+    alignas(16) uint16_t c[P * TC::PLANE];
+    alignas(16) Gates<L> g[2];
+  };
+  __shared__ Sh sh;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, m = lane & 15, q4 = lane >> 4;
+  int64_t u = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+  const int slab = (int)(u % g.slabs);
+  u /= g.slabs;
+  const int n = (int)(u % g.N);
+  u /= g.N;
+  const int64_t seg = u % g.nseg;
+  const int64_t bi = u / g.nseg;
+  const int64_t bn = bi * g.N + n;
+  const int c0 = slab * 64 * NT;
+  const bool rev = g.rev != 0;
+  const int64_t seg0 = seg * g.seglen;
+  const int64_t seg1 = seg0 + g.seglen < g.T ? seg0 + g.seglen : g.T;
+  const int nch = (int)((seg1 - seg0 + L - 1) / L);
+  const int64_t bh = g.N / g.b_grp, ch_ = g.N / g.c_grp;
+  const InT* pb = (const InT*)g.b + (bi * g.T * bh + n / g.b_grp) * g.DA;
+  const InT* pc = (const InT*)g.c + (bi * g.T * ch_ + n / g.c_grp) * g.DC + c0;
+  const int64_t sb = bh * g.DA, sc = ch_ * g.DC;
+  const float* pl = g.logit + bi * g.T * g.N + n;
+  const float alpha = g.alpha[n], beta = g.beta[n];
+  const int dc = g.DC - c0;
+  auto chunk_at = [&](int i) { return seg0 + (int64_t)(rev ? nch - 1 - i : i) * L; };
+  auto chunk_len = [&](int64_t t0) { return (int)(seg1 - t0 < L ? seg1 - t0 : L); };
+  const int step = rev ? -1 : 1;
+  auto first_tok = [&](int64_t t0, int len) { return rev ? t0 + len - 1 : t0; };
+  auto logit_of = [&](int i) {
+    const int64_t t0 = chunk_at(i);
+    const int len = chunk_len(t0);
+    return lane < len ? pl[(first_tok(t0, len) + step * lane) * g.N] : 0.0f;
+  };
+
+  f32x4 st[2 * AT][NT];
+#pragma unroll
+  for (int at = 0; at < 2 * AT; ++at)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) st[at][nt] = f32x4{0, 0, 0, 0};
+  float ftot = 1.0f;
+  TB fb;
+  TC fc;
+  float xl = 0.0f;
+  {
+    const int64_t t0 = chunk_at(0);
+    const int len = chunk_len(t0);
+    fb.fetch(pb, sb, first_tok(t0, len), step, len, g.DA, g.vb);
+    fc.fetch(pc, sc, first_tok(t0, len), step, len, dc, g.vc);
+    if (w == 3) {
+      const float x = logit_of(0);
+      if (nch > 1) xl = logit_of(1);
+      make_gates<L>(sh.g[0], x, alpha, beta, len, rev, g.w_in, false);
+    }
+    fb.put(sh.b);
+    fc.put(sh.c);
+  }
+  __syncthreads();
+  for (int ch = 0; ch < nch; ++ch) {
+    const Gates<L>& G = sh.g[ch & 1];
+    if (ch + 1 < nch) {
+      const int64_t t1 = chunk_at(ch + 1);
+      const int len1 = chunk_len(t1);
+      fb.fetch(pb, sb, first_tok(t1, len1), step, len1, g.DA, g.vb);
+      fc.fetch(pc, sc, first_tok(t1, len1), step, len1, dc, g.vc);
+      if (w == 3) {
+        make_gates<L>(sh.g[(ch + 1) & 1], xl, alpha, beta, len1, rev, g.w_in, false);
+        if (ch + 2 < nch) xl = logit_of(ch + 2);
+      }
+    }
+    const float f = G.total;
+    ftot *= f;
+#pragma unroll
+    for (int at = 0; at < 2 * AT; ++at)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) st[at][nt] *= f;
+#pragma unroll
+    for (int jb = 0; jb < L / 32; ++jb) {
+      bf16x8 cw[NT][3];
+      const f32x4 w0 = *(const f32x4*)(G.W + 32 * jb + 8 * q4),
+                  w1 = *(const f32x4*)(G.W + 32 * jb + 8 * q4 + 4);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        bf16x8 xc[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          xc[p] = col8(sh.c + p * TC::PLANE + (32 * jb + 8 * q4) * TC::STRIDE + 16 * (w * NT + nt),
+                       TC::STRIDE, m);
+        float x[8];
+        widen8<P>(xc, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= j < 4 ? w0[j & 3] : w1[j & 3];
+        split8<3>(x, cw[nt]);
+      }
+#pragma unroll
+      for (int at = 0; at < 2 * AT; ++at) {
+        bf16x8 xb[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          xb[p] = col8(sh.b + p * TB::PLANE + (32 * jb + 8 * q4) * TB::STRIDE + 16 * at, TB::STRIDE, m);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) st[at][nt] = mfma_terms(xb, cw[nt], st[at][nt]);
+      }
+    }
+    __syncthreads();
+    if (ch + 1 < nch) {
+      fb.put(sh.b);
+      fc.put(sh.c);
+      __syncthreads();
+    }
+  }
+  float* o = g.contrib + (bn * g.nseg + seg) * (int64_t)g.DA * g.DC;
+#pragma unroll
+  for (int at = 0; at < 2 * AT; ++at)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int ai = 16 * at + 4 * q4 + r, ci = c0 + 16 * (w * NT + nt) + m;
+        if (ai < g.DA && ci < g.DC) o[(int64_t)ai * g.DC + ci] = st[at][nt][r];
+      }
+  if (g.fseg && slab == 0 && threadIdx.x == 0) g.fseg[bn * g.nseg + seg] = ftot;
+}
+
+}  // namespace ssm
+}  // namespace m2rnn

@@ -387,3 +387,54 @@ def m2rnn_gate_rmsnorm_bwd(y, g_pre, gamma, dout, eps: float = 1e-6, workspace=N
                                            _ptr(dgamma), _ptr(ws), wsb, _stream(y.device))
     check(st, "m2rnn_gate_rmsnorm_bwd")
     return dy, dg, dgamma
+
+
+# ---- the selective state-space scan
+
+def _ssm_sizes(k, v, q, logit, alpha, beta, w_r, H0):
+    """Checks the scan's inputs; returns (B, T, N, NQ, K, V)."""
+    N, NQ = _heads(k, v)
+    B, T, _, K = k.shape
+    V = v.shape[-1]
+    f32 = torch.float32
+    _need(v, (B, T, N, V), k.dtype, "v")
+    _need(q, (B, T, NQ, K), k.dtype, "q")
+    _need(logit, (B, T, N), f32, "logit")
+    _need(alpha, (N,), f32, "alpha")
+    _need(beta, (N,), f32, "beta")
+    _need(w_r, (N, V), f32, "w_r")
+    _opt(H0, (B, N, K, V), f32, "H0")
+    return B, T, N, NQ, K, V
+
+
+def m2rnn_ssm_workspace_bytes(is_bwd: bool, B: int, T: int, n_heads: int, qk_heads: int, K: int,
+                              V: int, in_dtype=torch.bfloat16) -> int:
+    return int(_lib.lib().m2rnn_ssm_workspace_bytes(int(bool(is_bwd)), B, T, n_heads, qk_heads, K,
+                                                    V, _DT[in_dtype]))
+
+
+def m2rnn_ssm_fwd(k, v, q, logit, alpha, beta, w_r, H0=None, want_ht: bool = True, out=None,
+                  workspace=None):
+    """The selective state-space scan
+        d_t = softplus(logit_t + beta),  H_t = exp(-alpha d_t) H_{t-1} + d_t k_t v_t^T,
+        y_t = H_t^T q_t + w_r * v_t
+    over [B, T] tokens.  k, q [B, T, NQ, K] and v [B, T, N, V] in float32 or bfloat16 (NQ
+    divides N as in m2rnn_fwd); logit [B, T, N], alpha, beta [N], w_r [N, V] and H0
+    [B, N, K, V] float32.  Returns (y in v's dtype, HT float32 or None); ``out`` may hold
+    preallocated (y, HT).  logit = -inf makes a token leave the state alone."""
+    B, T, N, NQ, K, V = _ssm_sizes(k, v, q, logit, alpha, beta, w_r, H0)
+    dev = k.device
+    if out is not None:
+        y, HT = out
+    else:
+        y = torch.empty((B, T, N, V), dtype=v.dtype, device=dev)
+        HT = torch.empty((B, N, K, V), dtype=torch.float32, device=dev) if want_ht else None
+    _need(y, (B, T, N, V), v.dtype, "y")
+    _opt(HT, (B, N, K, V), torch.float32, "HT")
+    ws, wsb = _workspace(m2rnn_ssm_workspace_bytes(False, B, T, N, NQ, K, V, k.dtype), dev,
+                         workspace)
+    st = _lib.lib().m2rnn_ssm_fwd(B, T, N, NQ, K, V, _DT[k.dtype], _ptr(k), _ptr(v), _ptr(q),
+                                  _ptr(logit), _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(H0),
+                                  _ptr(y), _ptr(HT), _ptr(ws), wsb, _stream(dev))
+    check(st, "m2rnn_ssm_fwd")
+    return y, HT

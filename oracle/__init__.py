@@ -33,3 +33,4 @@ from .m2rnn_block import (  # noqa: F401
     gate_rmsnorm_backward,
 )
 from .m2rnn_newton import newton_forward, newton_linearize  # noqa: F401
+from .m2rnn_ssm import ssm_backward, ssm_forward, ssm_step  # noqa: F401
