@@ -377,6 +377,30 @@ int m2rnn_ssm_fwd(int64_t B, int64_t T, int64_t n_heads, int64_t qk_heads, int64
                   const void* alpha, const void* beta, const void* w_r, const void* H0, void* y,
                   void* HT, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * m2rnn_ssm_bwd -- gradients of m2rnn_ssm_fwd for a loss with dL/dy = dy and
+ * dL/dH_T = dHT.  With R_t the gradient of H_t (R_T = dHT + q_T dy_T^T,
+ * R_t = f_{t+1} R_{t+1} + q_t dy_t^T) and x = logit + beta:
+ *     dq_t = H_t dy_t,  dk_t = d_t R_t v_t,  dv_t = d_t R_t^T k_t + w_r (.) dy_t,
+ *     dd_t = k_t^T R_t v_t,  dl_t = f_t <H_{t-1}, R_t>  (with respect to log f_t),
+ *     dlogit_t = sigmoid(x_t) (dd_t - alpha dl_t),  dH_0 = f_1 R_1,
+ *     dw_r = sum dy (.) v,  dalpha = sum -d_t dl_t,  dbeta = sum dlogit_t   (over b and t).
+ * The states are recomputed; nothing of the forward call is needed.
+ *   k, v, q, logit, alpha, beta, w_r, H0   as for m2rnn_ssm_fwd
+ *   dy     [B, T, n_heads, V]   in, in_dtype
+ *   dHT    [B, n_heads, K, V]   in, or NULL for zero
+ *   dk, dq [B, T, qk_heads, K]  out, in_dtype (a shared head's sum over its group)
+ *   dv     [B, T, n_heads, V]   out, in_dtype
+ *   dlogit [B, T, n_heads]      out;  dw_r [n_heads, V] out;  dalpha, dbeta [n_heads] out
+ *   dH0    [B, n_heads, K, V]   out, or NULL to skip
+ */
+int m2rnn_ssm_bwd(int64_t B, int64_t T, int64_t n_heads, int64_t qk_heads, int64_t K, int64_t V,
+                  int in_dtype, const void* k, const void* v, const void* q, const void* logit,
+                  const void* alpha, const void* beta, const void* w_r, const void* H0,
+                  const void* dy, const void* dHT, void* dk, void* dv, void* dq, void* dlogit,
+                  void* dw_r, void* dalpha, void* dbeta, void* dH0, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -59,6 +59,9 @@ SIGNATURES = {
     "m2rnn_ssm_workspace_bytes": (_sz, [_int, _i64, _i64, _i64, _i64, _i64, _i64, _int]),
     "m2rnn_ssm_fwd": (_int, [_i64, _i64, _i64, _i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp,
                              _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "m2rnn_ssm_bwd": (_int, [_i64, _i64, _i64, _i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp,
+                             _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                             _vp, _sz, _vp]),
 }
 
 _lib = None

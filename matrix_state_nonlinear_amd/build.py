@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libm2rnn.so")
 SOURCES = ["m2rnn_api.hip", "m2rnn_gates.hip", "m2rnn_fwd.hip", "m2rnn_bwd.hip",
            "m2rnn_step.hip", "m2rnn_block.hip",
-           "m2rnn_newton.hip", "m2rnn_ssm.hip", "m2rnn_ssm_sweep.hip", "m2rnn_ssm_sweep_f32.hip"]
+           "m2rnn_newton.hip", "m2rnn_ssm.hip", "m2rnn_ssm_bwd.hip",
+           "m2rnn_ssm_sweep.hip", "m2rnn_ssm_sweep_f32.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 VALU instructions are switched off for every kernel.  MFMA

@@ -114,6 +114,18 @@ bool newton_supported(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
   return waves < 2.0e9 && map_waves < 2.0e9 && U * (double)T * (double)K * (double)V < 4.0e18;
 }
 
+// The state-space scan's shapes: the recurrence's, and grids of fewer than 2^32 threads in
+// the backward (segments x heads, two 128-column slabs at most, and one thread for each element of a
+// shared head's gradient).
+bool ssm_supported(int64_t B, int64_t T, int64_t N, int64_t NQ, int64_t K, int64_t V) {
+  if (!sizes_supported(B, T, N, K, V)) return false;
+  if (B * T * N == 0) return true;
+  const SsmLayout L = ssm_bwd_layout(B, T, N, NQ, K, V, M2RNN_F32);
+  return 2.0 * (double)B * (double)N * (double)L.nseg < (double)(1 << 24) &&
+         (double)B * (double)T * (double)NQ * (double)K < 4294967296.0 &&
+         (double)B * (double)N * (double)K * (double)V < 4294967296.0;
+}
+
 // The argument checks of m2rnn_bwd and m2rnn_bwd_noalloc, before any
 // workspace: M2RNN_OK or the status to return.
 int bwd_check(int64_t B, int64_t T, int64_t n_heads, int64_t qk_heads, int64_t K, int64_t V,
@@ -473,11 +485,12 @@ int m2rnn_gate_rmsnorm_bwd(int64_t rows, int64_t D, int io_dtype, int param_dtyp
 
 size_t m2rnn_ssm_workspace_bytes(int is_bwd, int64_t B, int64_t T, int64_t n_heads,
                                  int64_t qk_heads, int64_t K, int64_t V, int in_dtype) {
-  if (!sizes_ok(B, T, n_heads, K, V) || !qk_heads_ok(n_heads, qk_heads) || is_bwd ||
-      !dtypes_ok(in_dtype, M2RNN_F32) || !sizes_supported(B, T, n_heads, K, V) ||
+  if (!sizes_ok(B, T, n_heads, K, V) || !qk_heads_ok(n_heads, qk_heads) ||
+      !dtypes_ok(in_dtype, M2RNN_F32) || !ssm_supported(B, T, n_heads, qk_heads, K, V) ||
       B * T * n_heads == 0)
     return 0;
-  const SsmLayout L = ssm_fwd_layout(B, T, n_heads, K, V, in_dtype);
+  const SsmLayout L = is_bwd ? ssm_bwd_layout(B, T, n_heads, qk_heads, K, V, in_dtype)
+                             : ssm_fwd_layout(B, T, n_heads, K, V, in_dtype);
   return align_up(L.total_floats * 4, 256);
 }
 
@@ -491,7 +504,7 @@ int m2rnn_ssm_fwd(int64_t B, int64_t T, int64_t n_heads, int64_t qk_heads, int64
   const bool empty = B * T * n_heads == 0;
   if (!empty && (!k || !v || !q || !logit || !alpha || !beta || !w_r || !y))
     return M2RNN_ERR_INVALID_ARG;
-  if (!dtypes_ok(in_dtype, M2RNN_F32) || !sizes_supported(B, T, n_heads, K, V))
+  if (!dtypes_ok(in_dtype, M2RNN_F32) || !ssm_supported(B, T, n_heads, qk_heads, K, V))
     return M2RNN_ERR_UNSUPPORTED;
   const hipStream_t st = (hipStream_t)stream;
   if (empty) return status_of(fill(HT, H0, B * n_heads * K * V, M2RNN_F32, st));
@@ -506,6 +519,47 @@ int m2rnn_ssm_fwd(int64_t B, int64_t T, int64_t n_heads, int64_t qk_heads, int64
   a.y = y; a.HT = (float*)HT; a.ws = (float*)workspace;
   a.B = B; a.T = T; a.N = n_heads; a.NQ = qk_heads; a.K = K; a.V = V;
   return status_of(launch_ssm_fwd(a, in_dtype, st));
+}
+
+int m2rnn_ssm_bwd(int64_t B, int64_t T, int64_t n_heads, int64_t qk_heads, int64_t K, int64_t V,
+                  int in_dtype, const void* k, const void* v, const void* q, const void* logit,
+                  const void* alpha, const void* beta, const void* w_r, const void* H0,
+                  const void* dy, const void* dHT, void* dk, void* dv, void* dq, void* dlogit,
+                  void* dw_r, void* dalpha, void* dbeta, void* dH0, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  if (!sizes_ok(B, T, n_heads, K, V) || !qk_heads_ok(n_heads, qk_heads) ||
+      !in_dtype_known(in_dtype))
+    return M2RNN_ERR_INVALID_ARG;
+  const bool empty = B * T * n_heads == 0;
+  if (n_heads > 0 && (!dw_r || !dalpha || !dbeta)) return M2RNN_ERR_INVALID_ARG;
+  if (!empty && (!k || !v || !q || !logit || !alpha || !beta || !w_r || !dy || !dk || !dv || !dq ||
+                 !dlogit))
+    return M2RNN_ERR_INVALID_ARG;
+  if (!dtypes_ok(in_dtype, M2RNN_F32) || !ssm_supported(B, T, n_heads, qk_heads, K, V))
+    return M2RNN_ERR_UNSUPPORTED;
+  const hipStream_t st = (hipStream_t)stream;
+  if (empty) {  // sums over no tokens
+    hipError_t e = fill(dH0, dHT, B * n_heads * K * V, M2RNN_F32, st);
+    if (e == hipSuccess) e = fill(dw_r, nullptr, n_heads * V, M2RNN_F32, st);
+    if (e == hipSuccess) e = fill(dalpha, nullptr, n_heads, M2RNN_F32, st);
+    if (e == hipSuccess) e = fill(dbeta, nullptr, n_heads, M2RNN_F32, st);
+    return status_of(e);
+  }
+  const SsmLayout L = ssm_bwd_layout(B, T, n_heads, qk_heads, K, V, in_dtype);
+  const size_t need = align_up(L.total_floats * 4, 256);
+  if (!workspace || workspace_bytes < need) return M2RNN_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return M2RNN_ERR_INVALID_ARG;
+  SsmArgs a{};
+  a.k = k; a.v = v; a.q = q;
+  a.logit = (const float*)logit; a.alpha = (const float*)alpha; a.beta = (const float*)beta;
+  a.w_r = (const float*)w_r; a.H0 = (const float*)H0;
+  a.dy = dy; a.dHT = (const float*)dHT;
+  a.dk = dk; a.dv = dv; a.dq = dq;
+  a.dlogit = (float*)dlogit; a.dw_r = (float*)dw_r;
+  a.dalpha = (float*)dalpha; a.dbeta = (float*)dbeta; a.dH0 = (float*)dH0;
+  a.ws = (float*)workspace;
+  a.B = B; a.T = T; a.N = n_heads; a.NQ = qk_heads; a.K = K; a.V = V;
+  return status_of(launch_ssm_bwd(a, in_dtype, st));
 }
 
 }  // extern "C"

@@ -14,13 +14,16 @@ struct SsmSweepArgs {
   const void* a;        // [B, T, N / a_grp, DA]: head n reads head n / a_grp
   const void* b;        // [B, T, N / b_grp, DA]
   const void* c;        // [B, T, N / c_grp, DC]
-  const void* e;        // [B, T, N / e_grp, DC] or null: rowdot_p = e_p . (out_p / rho_p, no skip)
+  const void* e;        // [B, T, N / e_grp, DC] or null: rowdot_p = e_p . (R_p S^T a_p)
   const float* logit;   // [B, T, N]
   const float* alpha;   // [N]
   const float* beta;    // [N]
   const float* skip;    // [N, DC] or null
   void* out;            // [B, T, N, DC], input type, or fp32 when out_f32
   float* rowdot;        // [slabs, B, N, T] (e given)
+  float* pairs;         // [slabs, B, N, T] or null (e given): with M_ij = g_j D_ij (e_i . c_j)(a_i . b_j),
+                        // the sum of M over the chunk's pairs i >= p > j
+  float* colpairs;      // (pairs given) the sum of M_ip / g_p over the chunk's i >= p
   float* colsum;        // [B, N, nseg, DA] or null: sum_p a_p (.) b_p
   const float* state0;  // [B, N, nseg, *] segment starts (or [B, N, *] when nseg = 1), or null = 0
   float* stateT;        // [B, N, *] or null: the state after the last token (nseg = 1 only)
@@ -85,12 +88,15 @@ struct SsmArgs {
 struct SsmLayout {
   int64_t nseg, seglen;
   size_t hseg, fseg;                       // [B, N, nseg, K, V], [B, N, nseg] (nseg > 1 or backward)
-  size_t gseg, hT, base, udot, zdot;       // backward
+  size_t gseg, hT, base, adot, bdot, pairs, colpairs;  // backward
   size_t colsum, gatepart, dqp, dkp;
   size_t total_floats;
 };
 SsmLayout ssm_fwd_layout(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V, int in_dtype);
+SsmLayout ssm_bwd_layout(int64_t B, int64_t T, int64_t N, int64_t NQ, int64_t K, int64_t V,
+                         int in_dtype);
 hipError_t launch_ssm_fwd(const SsmArgs& a, int in_dtype, hipStream_t stream);
+hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream);
 
 // The sweep's instances, one input type per file (they compile in parallel).
 hipError_t launch_ssm_sweep_bf16(const SsmSweepArgs& a, hipStream_t stream);

@@ -13,6 +13,14 @@
 //     dk: a = v,  b = dy, c = q,  reverse, state R^T, d_p on the output
 // so one kernel computes all four.
 //
+// The gradient of the decays is taken from the same passes.  With M_ij = d_j 2^{c_i - c_j}
+// (q_i . k_j)(dy_i . v_j), H0 the state at the chunk's start and G the state gradient at its end,
+//     dl_t = f_t <H_{t-1}, R_t> = sum_{i >= t > j} M_ij + sum_{i >= t} a_i + sum_{j < t} b_j + 2^{c_L} <H0, G>,
+//     a_i = 2^{c_i} q_i^T H0 dy_i,   b_j = d_j 2^{c_L - c_j} k_j^T G v_j,   d_j dd_j = sum_{i >= j} M_ij + b_j:
+// the dq pass has the second factor of M and the parts a, and forms the first factor next to it
+// (its c and e tiles are k and q); the dk pass has b.  Nothing is subtracted inside a chunk, so a strong
+// decay does not cost precision.
+//
 // A workgroup (4 waves) walks one segment of one head, the state in MFMA
 // accumulators throughout: wave w owns 16 NT columns of it, all DA rows.  All
 // products use the 16x16x32 bf16 MFMA (16 times the rate of the fp32 one); bf16
@@ -20,11 +28,13 @@
 // the decayed inputs of the state update, and fp32 inputs) is split into bf16
 // terms whose sum is the fp32 value: three for what is summed into the state (24
 // bits, exact), two for the scores and the state's readout when the inputs and
-// outputs are bf16 (relative error 2^-17 against the output's 2^-9), three of them for
-// fp32 inputs.  Operands are taken so that an accumulator layout is the next
+// outputs are bf16 (relative error 2^-15 at most against the output's 2^-8), three of them for
+// fp32 inputs and where the readout goes into the decays' fp32 gradient.  Operands are taken so that an accumulator layout is the next
 // product's operand layout: the state's accumulators are the readout's operand without
 // a move, and an output lane holds four consecutive columns.
 #pragma once
+
+#include <type_traits>
 
 #include "m2rnn_device.h"
 #include "m2rnn_ssm_internal.h"
@@ -226,7 +236,8 @@ template <int L>
 struct Gates {
   float R[L];      // 2^{c_p}: from the carried state to p
   float W[L];      // 2^{c_end - c_p} g_p: from p to the state carried on
-  float eg[L];     // 2^{c_tile_end - c_p} g_p (tiles of 16 tokens)
+  float et[L];     // 2^{c_tile_end - c_p} (tiles of 16 tokens)
+  float eg[L];     // the same times g_p
   float rr[L / 16 - 1][L];  // 2^{c_p - c_end(tile j)}, j below p's tile
   float chi[L], clo[L];     // c_p in two parts, for the tiles on the diagonal
   float g[L];      // input weight
@@ -278,7 +289,9 @@ __device__ __forceinline__ void make_gates(Gates<L>& G, float x, float alpha, fl
   if (lane < L) {
     G.R[lane] = pow2(c);
     G.W[lane] = pow2(total - c) * g;
-    G.eg[lane] = pow2(tile_end - c) * g;
+    const float et = pow2(tile_end - c);
+    G.et[lane] = et;
+    G.eg[lane] = et * g;
 #pragma unroll
     for (int j = 0; j < L / 16 - 1; ++j) G.rr[j][lane] = rr[j];
     const float hi = (float)c;
@@ -291,7 +304,20 @@ __device__ __forceinline__ void make_gates(Gates<L>& G, float x, float alpha, fl
 }
 
 // ------------------------------------------------------------- the sweep
-template <typename InT, int AT, int NT>
+// What a sweep returns besides its output: nothing (y, dv); rowdot, the dot products of e with the
+// state's part of the output (dk: b / d); these (dq: a) and the sums over the pairs of a chunk.
+enum : int { kPlain = 0, kRowdot = 1, kPairs = 2 };
+
+// Sums over the pairs of a chunk, by 16 x 16 tile (it, jt) of M
+template <int L>
+struct PairSums {
+  alignas(16) float rs[L / 16][L];  // [jt][i] sum over the tile's j of M_ij, jt < i's tile
+  alignas(16) float cs[L / 16][L];  // [it][j] sum over the tile's i of M_ij / d_j, it >= j's tile
+  alignas(16) float xd[L];          // [t] sum over i >= t > j of t's own tile
+};
+struct NoSums {};
+
+template <typename InT, int AT, int NT, int MODE>
 struct SweepShared {
   using C = Cfg<InT>;
   static constexpr int L = C::L;
@@ -301,10 +327,47 @@ struct SweepShared {
   alignas(16) uint16_t a[C::planes * TA::PLANE];
   alignas(16) uint16_t b[C::planes * TA::PLANE];
   alignas(16) uint16_t c[C::planes * TC::PLANE];
+  alignas(16) uint16_t e[MODE == kPairs ? C::planes * TC::PLANE : 8];
   alignas(16) uint16_t p[C::score_terms][L * PSTRIDE];
   alignas(16) Gates<L> g[2];
   alignas(16) float red[4][L];
+  std::conditional_t<MODE == kPairs, PairSums<L>, NoSums> sums;
 };
+
+// Shifts within the 16-lane rows, zero beyond their ends: lane l reads lane l + N (l - N).
+template <int N>
+__device__ __forceinline__ float row_down(float x) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x100 + N, 0xF, 0xF, true));
+}
+template <int N>
+__device__ __forceinline__ float row_up(float x) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x110 + N, 0xF, 0xF, true));
+}
+// sum over the row's lanes from this one on
+__device__ __forceinline__ float row_suffix(float x) {
+  x += row_down<1>(x);
+  x += row_down<2>(x);
+  x += row_down<4>(x);
+  x += row_down<8>(x);
+  return x;
+}
+// sum over the row's lanes before this one
+__device__ __forceinline__ float row_prefix_excl(float x) {
+  x = row_up<1>(x);
+  x += row_up<1>(x);
+  x += row_up<2>(x);
+  x += row_up<4>(x);
+  x += row_up<8>(x);
+  return x;
+}
+// the sum of x over the four 16-lane rows, in every lane
+__device__ __forceinline__ float rows_sum(float x) {
+  x += __shfl_xor(x, 16);
+  x += __shfl_xor(x, 32);
+  return x;
+}
 
 template <typename InT>
 __device__ __forceinline__ void store_cols4(void* out, int64_t i, f32x4 x, int left, bool vec,
@@ -348,14 +411,15 @@ __device__ __forceinline__ f32x4 load_cols4(const InT* p, int left, bool vec) {
   return x;
 }
 
-template <typename InT, int AT, int NT>
+template <typename InT, int AT, int NT, int MODE>
 __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 1)
     m2rnn_ssm_sweep_kernel(const SsmSweepArgs g) {
   using C = Cfg<InT>;
-  using S = SweepShared<InT, AT, NT>;
+  using S = SweepShared<InT, AT, NT, MODE>;
   using TA = typename S::TA;
   using TC = typename S::TC;
-  constexpr int L = C::L, NI = L / 16, P = C::planes, PS = C::score_terms, PH = C::state_terms;
+  constexpr int L = C::L, NI = L / 16, P = C::planes, PS = C::score_terms,
+                PH = MODE == kPlain ? C::state_terms : 3;
   __shared__ S sh;
 
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, m = lane & 15, q4 = lane >> 4;
@@ -407,7 +471,7 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
     const float* he = nullptr;
     if (g.base)
       he = seg + 1 < g.nseg ? g.hend + (bn * g.nseg + seg + 1) * kv : g.hend_last + bn * kv;
-    float dot = 0.0f;
+    double dot = 0.0;
 #pragma unroll
     for (int at = 0; at < 2 * AT; ++at)
 #pragma unroll
@@ -419,22 +483,26 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
           const int64_t o = (int64_t)ai * g.a_stride + (int64_t)ci * g.c_stride;
           const float x = (s0 && ok) ? s0[o] : 0.0f;
           st[at][nt][r] = x;
-          if (he && ok) dot += x * he[o];
+          if (he && ok) dot += (double)x * (double)he[o];
         }
     if (g.base) {
 #pragma unroll
       for (int s = 1; s < 64; s *= 2) dot += __shfl_xor(dot, s);
-      if (lane == 0) sh.red[w][0] = dot;
+      double* red = (double*)&sh.red[0][0];
+      if (lane == 0) red[w] = dot;
       __syncthreads();
       if (threadIdx.x == 0)
         g.base[((int64_t)slab * g.B * g.N + bn) * g.nseg + seg] =
-            (sh.red[0][0] + sh.red[1][0]) + (sh.red[2][0] + sh.red[3][0]);
+            (float)((red[0] + red[1]) + (red[2] + red[3]));
       __syncthreads();
     }
   }
 
   TA fa, fb;
-  TC fc;
+  TC fc, fe;
+  const int64_t eh = g.N / g.e_grp;
+  const InT* pe = (const InT*)g.e + (bi * g.T * eh + n / g.e_grp) * g.DC + c0;
+  const int64_t se = eh * g.DC;
   float csum[C::epc];
 #pragma unroll
   for (int j = 0; j < C::epc; ++j) csum[j] = 0.0f;
@@ -447,6 +515,7 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
     fa.fetch(pa, sa, first_tok(t0, len), step, len, g.DA, g.va);
     fb.fetch(pb, sb, first_tok(t0, len), step, len, g.DA, g.vb);
     fc.fetch(pc, sc, first_tok(t0, len), step, len, dc, g.vc);
+    if constexpr (MODE == kPairs) fe.fetch(pe, se, first_tok(t0, len), step, len, dc, g.ve);
     if (w == 3) {
       const float x = logit_of(0);
       if (nch > 1) xl = logit_of(1);
@@ -455,6 +524,7 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
     fa.put(sh.a);
     fb.put(sh.b);
     fc.put(sh.c);
+    if constexpr (MODE == kPairs) fe.put(sh.e);
     if (do_col) TA::dot_cols(fa, fb, csum);
   }
   __syncthreads();
@@ -469,6 +539,7 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
       fa.fetch(pa, sa, first_tok(t1, len1), step, len1, g.DA, g.va);
       fb.fetch(pb, sb, first_tok(t1, len1), step, len1, g.DA, g.vb);
       fc.fetch(pc, sc, first_tok(t1, len1), step, len1, dc, g.vc);
+      if constexpr (MODE == kPairs) fe.fetch(pe, se, first_tok(t1, len1), step, len1, dc, g.ve);
     }
 
     // scores: tile (it, jt), jt <= it, of a b^T, decayed and split.  Waves 0..2 take every
@@ -495,21 +566,58 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
         }
         // lane: token i = 16 it + m, inputs j = 16 jt + 4 q4 + r
         const int i = 16 * it + m, j0 = 16 * jt + 4 * q4;
+        f32x4 g4{1, 1, 1, 1};  // input weights not yet in s
         if (it == jt) {
-          const f32x4 ch4 = *(const f32x4*)(G.chi + j0), cl4 = *(const f32x4*)(G.clo + j0),
-                      g4 = *(const f32x4*)(G.g + j0);
+          const f32x4 ch4 = *(const f32x4*)(G.chi + j0), cl4 = *(const f32x4*)(G.clo + j0);
+          g4 = *(const f32x4*)(G.g + j0);
           const float hi = G.chi[i], lo = G.clo[i];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float dec = __builtin_amdgcn_exp2f((hi - ch4[r]) + (lo - cl4[r])) * g4[r];
+            const float dec = __builtin_amdgcn_exp2f((hi - ch4[r]) + (lo - cl4[r]));
             s[r] = j0 + r <= i ? s[r] * dec : 0.0f;
           }
         } else {
-          const f32x4 e4 = *(const f32x4*)(G.eg + j0);
+          const f32x4 e4 = *(const f32x4*)((MODE == kPairs ? G.et : G.eg) + j0);
+          if constexpr (MODE == kPairs) g4 = *(const f32x4*)(G.g + j0);
           const float ri = G.rr[jt][i];
 #pragma unroll
           for (int r = 0; r < 4; ++r) s[r] *= ri * e4[r];
         }
+        if constexpr (MODE == kPairs) {
+          // the other factor of M: c . e (k . q)
+          f32x4 qk{0, 0, 0, 0};
+          const uint16_t* re = sh.e + (16 * it + m) * TC::STRIDE + 8 * q4;
+          const uint16_t* rc = sh.c + (16 * jt + m) * TC::STRIDE + 8 * q4;
+#pragma unroll
+          for (int t = 0; t < 2 * NT; ++t) {
+            bf16x8 xe[P], xc[P];
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+              xe[p] = row8(re + p * TC::PLANE + 32 * t);
+              xc[p] = row8(rc + p * TC::PLANE + 32 * t);
+            }
+            qk = mfma_terms(xc, xe, qk);
+          }
+          f32x4 mm = s * qk, col;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) col[r] = row16_sum(mm[r]);
+          if (m == 0) *(f32x4*)(sh.sums.cs[it] + j0) = col;
+          mm *= g4;
+          float sum = 0.0f;
+          if (it == jt) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float suf = row_suffix(mm[r]);
+              sum += j0 + r < i ? suf : 0.0f;
+            }
+            sum = rows_sum(sum);
+            if (q4 == 0) sh.sums.xd[i] = sum;
+          } else {
+            sum = rows_sum((mm[0] + mm[1]) + (mm[2] + mm[3]));
+            if (q4 == 0) sh.sums.rs[jt][i] = sum;
+          }
+        }
+        if (MODE == kPairs || it == jt) s *= g4;
         uint32_t x0[PS], x1[PS];
         split2<PS>(s[0], s[1], x0);
         split2<PS>(s[2], s[3], x1);
@@ -555,7 +663,66 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) acc[it][nt] *= R;
     }
+    if constexpr (MODE != kPlain) {
+      // e . (the state's part of the output), this wave's columns
+#pragma unroll
+      for (int it = 0; it < NI; ++it) {
+        const int i = 16 * it + m;
+        float dot = 0.0f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int cc = 16 * (w * NT + nt) + 4 * q4, left = dc - cc;
+          f32x4 ev{0, 0, 0, 0};
+          if constexpr (MODE == kPairs) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+              const u32x2 uu = *(const u32x2*)(sh.e + p * TC::PLANE + i * TC::STRIDE + cc);
+              ev += f32x4{lo_half(uu[0]), hi_half(uu[0]), lo_half(uu[1]), hi_half(uu[1])};
+            }
+          } else if (i < len && left > 0) {
+            ev = load_cols4(pe + (first_tok(t0, len) + step * i) * se + cc, left, g.ve);
+          }
+          const f32x4 x = acc[it][nt];
+          dot += (ev[0] * x[0] + ev[1] * x[1]) + (ev[2] * x[2] + ev[3] * x[3]);
+        }
+        dot = rows_sum(dot);
+        if (q4 == 0) sh.red[w][i] = dot;
+      }
+    }
     __syncthreads();  // the scores are in LDS
+
+    if constexpr (MODE != kPlain) {
+      if (w == 2 && lane < len) {
+        const int64_t o = ((int64_t)slab * g.B * g.N + bn) * g.T + first_tok(t0, len) + step * lane;
+        g.rowdot[o] = (sh.red[0][lane] + sh.red[1][lane]) + (sh.red[2][lane] + sh.red[3][lane]);
+      }
+    }
+    if constexpr (MODE == kPairs) {
+      if (w == 3) {
+        // per token t: all pairs i >= t > j of the chunk, from the tiles' sums; and sum_i M_it / d_t
+        const int t = lane & (L - 1), tt = t >> 4;
+        float row[NI - 1], rowtot = 0.0f, coltot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NI - 1; ++j) {
+          row[j] = tt > j ? sh.sums.rs[j][t] : 0.0f;
+          rowtot += row[j];
+        }
+#pragma unroll
+        for (int it = NI - 1; it > 0; --it) coltot += it > tt ? sh.sums.cs[it][t] : 0.0f;
+        float x = sh.sums.xd[t] + row_suffix(rowtot) + row_prefix_excl(coltot * G.g[t]);
+        if constexpr (NI == 4) {  // tiles on both sides of t's
+          const float t0s = row16_sum(row[0]), t1s = row16_sum(row[1]);
+          const float s20 = lane_value_r(t0s, 32), s30 = lane_value_r(t0s, 48),
+                      s31 = lane_value_r(t1s, 48);
+          x += tt == 1 ? s20 + s30 : tt == 2 ? s30 + s31 : 0.0f;
+        }
+        if (lane < len) {
+          const int64_t o = ((int64_t)slab * g.B * g.N + bn) * g.T + first_tok(t0, len) + step * lane;
+          g.pairs[o] = x;
+          g.colpairs[o] = coltot + sh.sums.cs[tt][t];
+        }
+      }
+    }
 
     // the chunk's own inputs, and what they leave in the state
     const float ftot = G.total;
@@ -606,18 +773,11 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
       const int i = 16 * it + m;
       const bool ok = i < len;
       const int64_t tok = first_tok(t0, len) + step * i;
-      float dot = 0.0f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int cc = 16 * (w * NT + nt) + 4 * q4;
         f32x4 x = acc[it][nt];
         const int left = dc - cc;
-        if (g.e && ok && left > 0) {
-          const InT* pe = (const InT*)g.e +
-                          ((bi * g.T + tok) * (g.N / g.e_grp) + n / g.e_grp) * g.DC + c0 + cc;
-          const f32x4 ev = load_cols4(pe, left, g.ve);
-          dot += (ev[0] * x[0] + ev[1] * x[1]) + (ev[2] * x[2] + ev[3] * x[3]);
-        }
         x *= G.rho[i];
         if (g.skip && left > 0) {
           f32x4 cv{0, 0, 0, 0};
@@ -635,22 +795,13 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
           store_cols4<InT>(g.out, ((bi * g.T + tok) * g.N + n) * g.DC + c0 + cc, x, left, g.vo,
                            g.out_f32);
       }
-      if (g.e) {
-        dot += __shfl_xor(dot, 16);
-        dot += __shfl_xor(dot, 32);
-        if (q4 == 0) sh.red[w][i] = dot;
-      }
     }
     __syncthreads();  // everybody is done with the tiles
-    if (g.e && threadIdx.x < L && (int)threadIdx.x < len) {
-      const int i = threadIdx.x;
-      g.rowdot[((int64_t)slab * g.B * g.N + bn) * g.T + first_tok(t0, len) + step * i] =
-          (sh.red[0][i] + sh.red[1][i]) + (sh.red[2][i] + sh.red[3][i]);
-    }
     if (ch + 1 < nch) {
       fa.put(sh.a);
       fb.put(sh.b);
       fc.put(sh.c);
+      if constexpr (MODE == kPairs) fe.put(sh.e);
       if (do_col) TA::dot_cols(fa, fb, csum);
       __syncthreads();
     }

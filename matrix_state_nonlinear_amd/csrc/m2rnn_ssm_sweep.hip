@@ -4,36 +4,45 @@
 namespace m2rnn {
 namespace {
 
-template <typename InT, int AT, int NT>
+template <typename InT, int AT, int NT, int MODE>
 hipError_t run(const SsmSweepArgs& a, hipStream_t stream) {
   const int64_t grid = a.B * a.N * a.nseg * a.slabs;
-  hipLaunchKernelGGL((ssm::m2rnn_ssm_sweep_kernel<InT, AT, NT>), dim3((unsigned)grid), dim3(256),
-                     0, stream, a);
+  hipLaunchKernelGGL((ssm::m2rnn_ssm_sweep_kernel<InT, AT, NT, MODE>), dim3((unsigned)grid),
+                     dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
-template <typename InT, int AT>
+template <typename InT, int AT, int MODE>
 hipError_t pick_nt(const SsmSweepArgs& a, hipStream_t stream) {
-  return a.DC <= 64 ? run<InT, AT, 1>(a, stream) : run<InT, AT, 2>(a, stream);
+  return a.DC <= 64 ? run<InT, AT, 1, MODE>(a, stream) : run<InT, AT, 2, MODE>(a, stream);
+}
+
+template <typename InT, int MODE>
+hipError_t pick_at(const SsmSweepArgs& a, hipStream_t stream) {
+  if (a.DA <= 32) return pick_nt<InT, 1, MODE>(a, stream);
+  if (a.DA <= 64) return pick_nt<InT, 2, MODE>(a, stream);
+  if (a.DA <= 128) return pick_nt<InT, 4, MODE>(a, stream);
+  // only y and dv contract over K; dq and dk contract over V <= 128
+  if constexpr (MODE == ssm::kPlain) return pick_nt<InT, 8, MODE>(a, stream);
+  return hipErrorInvalidValue;
 }
 
 template <typename InT>
-hipError_t pick_at(const SsmSweepArgs& a, hipStream_t stream) {
-  if (a.DA <= 32) return pick_nt<InT, 1>(a, stream);
-  if (a.DA <= 64) return pick_nt<InT, 2>(a, stream);
-  if (a.DA <= 128) return pick_nt<InT, 4>(a, stream);
-  return pick_nt<InT, 8>(a, stream);
+hipError_t pick_mode(const SsmSweepArgs& a, hipStream_t stream) {
+  if (a.pairs) return pick_at<InT, ssm::kPairs>(a, stream);
+  if (a.e) return pick_at<InT, ssm::kRowdot>(a, stream);
+  return pick_at<InT, ssm::kPlain>(a, stream);
 }
 
 }  // namespace
 
 #ifdef M2RNN_SSM_F32
 hipError_t launch_ssm_sweep_f32(const SsmSweepArgs& a, hipStream_t stream) {
-  return pick_at<float>(a, stream);
+  return pick_mode<float>(a, stream);
 }
 #else
 hipError_t launch_ssm_sweep_bf16(const SsmSweepArgs& a, hipStream_t stream) {
-  return pick_at<uint16_t>(a, stream);
+  return pick_mode<uint16_t>(a, stream);
 }
 #endif
 

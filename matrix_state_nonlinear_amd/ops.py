@@ -438,3 +438,41 @@ def m2rnn_ssm_fwd(k, v, q, logit, alpha, beta, w_r, H0=None, want_ht: bool = Tru
                                   _ptr(y), _ptr(HT), _ptr(ws), wsb, _stream(dev))
     check(st, "m2rnn_ssm_fwd")
     return y, HT
+
+
+def m2rnn_ssm_bwd(k, v, q, logit, alpha, beta, w_r, H0, dy, dHT=None, want_dh0: bool = True,
+                  workspace=None, out=None):
+    """Backward of m2rnn_ssm_fwd: a dict with dk, dv, dq (k's dtype), dlogit, dw_r, dalpha,
+    dbeta and dH0 (or None) in float32.  dy [B, T, N, V] in v's dtype, dHT [B, N, K, V] float32
+    or None.  ``out`` may hold preallocated buffers under those names (any missing one is
+    allocated; dH0 = None there skips it)."""
+    B, T, N, NQ, K, V = _ssm_sizes(k, v, q, logit, alpha, beta, w_r, H0)
+    f32 = torch.float32
+    _need(dy, (B, T, N, V), v.dtype, "dy")
+    _opt(dHT, (B, N, K, V), f32, "dHT")
+    dev = k.device
+    spec = {"dk": ((B, T, NQ, K), k.dtype), "dv": ((B, T, N, V), k.dtype),
+            "dq": ((B, T, NQ, K), k.dtype), "dlogit": ((B, T, N), f32), "dw_r": ((N, V), f32),
+            "dalpha": ((N,), f32), "dbeta": ((N,), f32),
+            "dH0": ((B, N, K, V), f32) if want_dh0 else None}
+    given = dict(out) if out is not None else {}
+    o = {}
+    for name, sd in spec.items():
+        if name in given:
+            o[name] = given[name]
+            if sd is None:
+                if o[name] is not None:
+                    raise ValueError("dH0 given with want_dh0=False")
+            else:
+                (_opt if name == "dH0" else _need)(o[name], sd[0], sd[1], name)
+        else:
+            o[name] = None if sd is None else torch.empty(sd[0], dtype=sd[1], device=dev)
+    ws, wsb = _workspace(m2rnn_ssm_workspace_bytes(True, B, T, N, NQ, K, V, k.dtype), dev,
+                         workspace)
+    st = _lib.lib().m2rnn_ssm_bwd(
+        B, T, N, NQ, K, V, _DT[k.dtype], _ptr(k), _ptr(v), _ptr(q), _ptr(logit), _ptr(alpha),
+        _ptr(beta), _ptr(w_r), _ptr(H0), _ptr(dy), _ptr(dHT), _ptr(o["dk"]), _ptr(o["dv"]),
+        _ptr(o["dq"]), _ptr(o["dlogit"]), _ptr(o["dw_r"]), _ptr(o["dalpha"]), _ptr(o["dbeta"]),
+        _ptr(o["dH0"]), _ptr(ws), wsb, _stream(dev))
+    check(st, "m2rnn_ssm_bwd")
+    return o
