@@ -401,6 +401,96 @@ int m2rnn_ssm_bwd(int64_t B, int64_t T, int64_t n_heads, int64_t qk_heads, int64
                   void* dw_r, void* dalpha, void* dbeta, void* dH0, void* workspace,
                   size_t workspace_bytes, void* stream);
 
+/*
+ * m2rnn_ssm_step -- one token of every sequence (decoding): the state is updated in place
+ * by one step of the scan and read out.  The same arithmetic as m2rnn_ssm_fwd in another order of
+ * the sums.
+ *   k, q   [B, qk_heads, K]     in, in_dtype
+ *   v      [B, n_heads, V]      in, in_dtype
+ *   logit  [B, n_heads]         in;  alpha, beta, w_r as for m2rnn_ssm_fwd
+ *   H      [B, n_heads, K, V]   in/out: H_{t-1} on entry, H_t on return
+ *   y      [B, n_heads, V]      out, in_dtype
+ * No workspace.  B * n_heads < 2^24 (else M2RNN_ERR_UNSUPPORTED); B * n_heads = 0 reads and writes
+ * nothing.
+ */
+int m2rnn_ssm_step(int64_t B, int64_t n_heads, int64_t qk_heads, int64_t K, int64_t V, int in_dtype,
+                   const void* k, const void* v, const void* q, const void* logit,
+                   const void* alpha, const void* beta, const void* w_r, void* H, void* y,
+                   void* stream);
+
+/*
+ * The block's short convolution with a history carried between calls, for prompts (whole or in
+ * pieces), truncated training windows and single tokens (m2rnn_conv_silu starts every
+ * sequence without history):
+ *     out_t[c] = SiLU(u_t[c]),  u_t[c] = bias[c] + sum_{i=0..3} w[c][i] x_{t-3+i}[c],
+ * where x_{-3}, x_{-2}, x_{-1} are hist's rows 0, 1, 2.  io_dtype F32 or BF16 is the type of x, out,
+ * hist, dout, dx and dhist (bf16 results are rounded to nearest even once); w, bias, dw and
+ * dbias are F32, and so is the arithmetic.
+ *
+ * m2rnn_conv_carry
+ *   x        [B, T, C]  in, io_dtype
+ *   w        [C, 4]     in;  bias [C] in, or NULL for none
+ *   hist     [B, 3, C]  in, io_dtype, oldest first, or NULL for zero
+ *   lens     [B]        in, int32, or NULL: how many of each sequence's T inputs count for
+ *                       hist_out (a padded batch); values outside [0, T] are taken as the nearest end
+ *   out      [B, T, C]  out, io_dtype (also behind lens)
+ *   hist_out [B, 3, C]  out, io_dtype, or NULL (then lens must be NULL): the last three inputs,
+ *                       hist's included where there are fewer than three; T = 0 copies hist
+ */
+int m2rnn_conv_carry(int64_t B, int64_t T, int64_t C, int io_dtype, const void* x, const void* w,
+                     const void* bias, const void* hist, const void* lens, void* out,
+                     void* hist_out, void* stream);
+
+/*
+ * m2rnn_conv_carry_bwd -- gradients of sum(dout * out), as m2rnn_conv_silu_bwd's, with
+ * dhist [B, 3, C] (io_dtype, or NULL; only where hist is given) that of the history.  A
+ * gradient of hist_out is not taken: between windows a caller adds the next one's dhist to
+ * the last three rows of dx.  dbias non-NULL exactly when bias is.
+ *   workspace / workspace_bytes: at least m2rnn_conv_carry_workspace_bytes(B, T, C), 16-byte aligned
+ */
+size_t m2rnn_conv_carry_workspace_bytes(int64_t B, int64_t T, int64_t C);
+int m2rnn_conv_carry_bwd(int64_t B, int64_t T, int64_t C, int io_dtype, const void* x,
+                         const void* w, const void* bias, const void* hist, const void* dout,
+                         void* dx, void* dw, void* dbias, void* dhist, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * m2rnn_conv_step -- one token of every sequence: out from hist and x, and hist [B, 3, C]
+ * shifted by x in place.
+ *   x, out [B, C]  io_dtype;  w, bias as above
+ */
+int m2rnn_conv_step(int64_t B, int64_t C, int io_dtype, const void* x, const void* w,
+                    const void* bias, void* hist, void* out, void* stream);
+
+/*
+ * m2rnn_groupnorm_gate -- an epilogue with a norm per head instead of per token: group norm
+ * over the channels of a token, then the SiLU gate,
+ *     out = (gamma (.) z + beta) (.) SiLU(g_pre),  z = (y - mean) / sqrt(var + eps),
+ * mean and (biased) variance over each of `groups` runs of D / groups consecutive channels
+ * (groups = n_heads normalises every head's V values by themselves; groups must divide D).
+ * io_dtype F32 or BF16 is the type of y, g_pre, out, dout, dy and dg_pre; gamma, beta [D] and
+ * their gradients are F32, and so are the statistics.
+ *   y, g_pre [rows, D]  in;  gamma, beta [D] in;  eps >= 0;  out [rows, D] out
+ */
+int m2rnn_groupnorm_gate(int64_t rows, int64_t D, int64_t groups, int io_dtype, double eps,
+                         const void* y, const void* g_pre, const void* gamma, const void* beta,
+                         void* out, void* stream);
+
+/*
+ * m2rnn_groupnorm_gate_bwd -- gradients of sum(dout * out): with a = gamma z + beta,
+ * da = dout SiLU(g_pre), dz = da gamma and means over the group:
+ *     dy = (dz - mean(dz) - z mean(dz z)) / sqrt(var + eps),  dg_pre = dout a SiLU'(g_pre),
+ *     dgamma = sum_rows da z,  dbeta = sum_rows da.
+ *   dout [rows, D] in;  dy, dg_pre [rows, D] out;  dgamma, dbeta [D] out
+ *   workspace / workspace_bytes: at least m2rnn_groupnorm_workspace_bytes(...), 16-byte aligned
+ */
+size_t m2rnn_groupnorm_workspace_bytes(int64_t rows, int64_t D, int64_t groups, int io_dtype);
+int m2rnn_groupnorm_gate_bwd(int64_t rows, int64_t D, int64_t groups, int io_dtype, double eps,
+                             const void* y, const void* g_pre, const void* gamma,
+                             const void* beta, const void* dout, void* dy, void* dg_pre,
+                             void* dgamma, void* dbeta, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,4 +13,7 @@ from .ops import (m2rnn_bwd, m2rnn_fwd, m2rnn_gates, m2rnn_step, m2rnn_workspace
                   m2rnn_status_string)
 from .ops import m2rnn_newton_fwd, m2rnn_newton_workspace_bytes  # noqa: F401
 from .ops import m2rnn_bwd_noalloc  # noqa: F401
-from .ops import m2rnn_ssm_bwd, m2rnn_ssm_fwd, m2rnn_ssm_workspace_bytes  # noqa: F401
+from .ops import (m2rnn_ssm_bwd, m2rnn_ssm_fwd, m2rnn_ssm_step,  # noqa: F401
+                  m2rnn_ssm_workspace_bytes)
+from .ops import m2rnn_conv_carry, m2rnn_conv_carry_bwd, m2rnn_conv_step  # noqa: F401
+from .ops import m2rnn_groupnorm_gate, m2rnn_groupnorm_gate_bwd  # noqa: F401

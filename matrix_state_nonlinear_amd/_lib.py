@@ -62,6 +62,18 @@ SIGNATURES = {
     "m2rnn_ssm_bwd": (_int, [_i64, _i64, _i64, _i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp,
                              _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                              _vp, _sz, _vp]),
+    "m2rnn_ssm_step": (_int, [_i64, _i64, _i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp,
+                              _vp, _vp, _vp, _vp]),
+    "m2rnn_conv_carry_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "m2rnn_conv_carry": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "m2rnn_conv_carry_bwd": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                    _vp, _vp, _vp, _sz, _vp]),
+    "m2rnn_conv_step": (_int, [_i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "m2rnn_groupnorm_workspace_bytes": (_sz, [_i64, _i64, _i64, _int]),
+    "m2rnn_groupnorm_gate": (_int, [_i64, _i64, _i64, _int, ctypes.c_double, _vp, _vp, _vp, _vp,
+                                    _vp, _vp]),
+    "m2rnn_groupnorm_gate_bwd": (_int, [_i64, _i64, _i64, _int, ctypes.c_double, _vp, _vp, _vp,
+                                        _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
 _lib = None

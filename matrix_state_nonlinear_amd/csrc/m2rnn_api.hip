@@ -101,6 +101,29 @@ hipError_t fill(void* dst, const void* src, int64_t n, int state_dtype, hipStrea
   return hipGetLastError();
 }
 
+// The same for 16-bit elements (a bf16 zero is all bits zero).
+__global__ void __launch_bounds__(256) fill16_kernel(uint16_t* __restrict__ dst,
+                                                     const uint16_t* __restrict__ src, int64_t n) {
+  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride)
+    dst[i] = src ? src[i] : (uint16_t)0;
+}
+
+hipError_t fill16(void* dst, const void* src, int64_t n, hipStream_t stream) {
+  if (!dst || n <= 0) return hipSuccess;
+  int64_t blocks = (n + 255) / 256;
+  if (blocks > 4096) blocks = 4096;
+  hipLaunchKernelGGL(fill16_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, (uint16_t*)dst,
+                     (const uint16_t*)src, n);
+  return hipGetLastError();
+}
+
+// The carried convolution's grids, at one channel per thread: below 2^32 threads.
+bool carry_grid_ok(int64_t B, int64_t T, int64_t C) {
+  const double runs = (double)B * ((double)T / 16.0 + 1.0) + 4.0;
+  return runs * ((double)C + 64.0) < 4.2e9 && 5.0 * (double)C / 64.0 < (double)(1 << 22);
+}
+
 // The Newton forward's shapes: V a multiple of 16 up to 64, and wave counts of
 // its kernels within 32-bit wave indices.
 bool newton_supported(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
@@ -560,6 +583,151 @@ int m2rnn_ssm_bwd(int64_t B, int64_t T, int64_t n_heads, int64_t qk_heads, int64
   a.ws = (float*)workspace;
   a.B = B; a.T = T; a.N = n_heads; a.NQ = qk_heads; a.K = K; a.V = V;
   return status_of(launch_ssm_bwd(a, in_dtype, st));
+}
+
+int m2rnn_ssm_step(int64_t B, int64_t n_heads, int64_t qk_heads, int64_t K, int64_t V, int in_dtype,
+                   const void* k, const void* v, const void* q, const void* logit,
+                   const void* alpha, const void* beta, const void* w_r, void* H, void* y,
+                   void* stream) {
+  if (!sizes_ok(B, 1, n_heads, K, V) || !qk_heads_ok(n_heads, qk_heads) ||
+      !in_dtype_known(in_dtype))
+    return M2RNN_ERR_INVALID_ARG;
+  const bool empty = B * n_heads == 0;
+  if (!empty && (!k || !v || !q || !logit || !alpha || !beta || !w_r || !H || !y))
+    return M2RNN_ERR_INVALID_ARG;
+  if (!dtypes_ok(in_dtype, M2RNN_F32) || K > 256 || V > 128 ||
+      (double)B * (double)n_heads >= (double)(1 << 24))
+    return M2RNN_ERR_UNSUPPORTED;
+  if (empty) return M2RNN_OK;  // no unit: nothing is read or written
+  SsmStepArgs a{};
+  a.k = k; a.v = v; a.q = q;
+  a.logit = (const float*)logit; a.alpha = (const float*)alpha; a.beta = (const float*)beta;
+  a.w_r = (const float*)w_r; a.H = (float*)H; a.y = y;
+  a.B = B; a.N = n_heads; a.NQ = qk_heads; a.K = K; a.V = V;
+  return status_of(launch_ssm_step(a, in_dtype, (hipStream_t)stream));
+}
+
+// ---- the convolution with a carried history
+
+size_t m2rnn_conv_carry_workspace_bytes(int64_t B, int64_t T, int64_t C) {
+  if (B < 0 || T < 0 || C < 1 || !carry_grid_ok(B, T, C) || B * T == 0) return 0;
+  return align_up(conv_carry_workspace_floats(B, T, C) * 4, 256);
+}
+
+int m2rnn_conv_carry(int64_t B, int64_t T, int64_t C, int io_dtype, const void* x, const void* w,
+                     const void* bias, const void* hist, const void* lens, void* out,
+                     void* hist_out, void* stream) {
+  if (B < 0 || T < 0 || C < 1 || !in_dtype_known(io_dtype)) return M2RNN_ERR_INVALID_ARG;
+  if (B * T > 0 && (!x || !w || !out)) return M2RNN_ERR_INVALID_ARG;
+  if (lens && !hist_out) return M2RNN_ERR_INVALID_ARG;
+  if (!dtypes_ok(io_dtype, M2RNN_F32) || !carry_grid_ok(B, T, C)) return M2RNN_ERR_UNSUPPORTED;
+  const hipStream_t st = (hipStream_t)stream;
+  if (B * T == 0) {  // no new input: the history goes on
+    const int64_t n = B * 3 * C;
+    if (io_dtype == M2RNN_F32) return status_of(fill(hist_out, hist, n, M2RNN_F32, st));
+    return status_of(fill16(hist_out, hist, n, st));
+  }
+  CarryArgs a{};
+  a.B = B; a.T = T; a.C = C; a.x = x; a.w = (const float*)w; a.bias = (const float*)bias;
+  a.hist = hist; a.lens = (const int*)lens; a.out = out; a.hist_out = hist_out;
+  return status_of(launch_conv_carry(a, io_dtype, 0, st));
+}
+
+int m2rnn_conv_carry_bwd(int64_t B, int64_t T, int64_t C, int io_dtype, const void* x,
+                         const void* w, const void* bias, const void* hist, const void* dout,
+                         void* dx, void* dw, void* dbias, void* dhist, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  if (B < 0 || T < 0 || C < 1 || !in_dtype_known(io_dtype)) return M2RNN_ERR_INVALID_ARG;
+  if (!w || !dw || (bias == nullptr) != (dbias == nullptr) || (dhist && !hist))
+    return M2RNN_ERR_INVALID_ARG;
+  if (B * T > 0 && (!x || !dout || !dx)) return M2RNN_ERR_INVALID_ARG;
+  if (!dtypes_ok(io_dtype, M2RNN_F32) || !carry_grid_ok(B, T, C)) return M2RNN_ERR_UNSUPPORTED;
+  const hipStream_t st = (hipStream_t)stream;
+  if (B * T == 0) {  // sums over no tokens
+    hipError_t e = fill(dw, nullptr, C * 4, M2RNN_F32, st);
+    if (e == hipSuccess) e = fill(dbias, nullptr, C, M2RNN_F32, st);
+    const int64_t n = B * 3 * C;
+    if (e == hipSuccess)
+      e = io_dtype == M2RNN_F32 ? fill(dhist, nullptr, n, M2RNN_F32, st)
+                                : fill16(dhist, nullptr, n, st);
+    return status_of(e);
+  }
+  const size_t need = m2rnn_conv_carry_workspace_bytes(B, T, C);
+  if (!workspace || workspace_bytes < need) return M2RNN_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return M2RNN_ERR_INVALID_ARG;
+  CarryArgs a{};
+  a.B = B; a.T = T; a.C = C; a.x = x; a.w = (const float*)w; a.bias = (const float*)bias;
+  a.hist = hist; a.dout = dout; a.dx = dx; a.dw = (float*)dw; a.dbias = (float*)dbias;
+  a.dhist = dhist; a.ws = (float*)workspace;
+  return status_of(launch_conv_carry(a, io_dtype, 1, st));
+}
+
+int m2rnn_conv_step(int64_t B, int64_t C, int io_dtype, const void* x, const void* w,
+                    const void* bias, void* hist, void* out, void* stream) {
+  if (B < 0 || C < 1 || !in_dtype_known(io_dtype)) return M2RNN_ERR_INVALID_ARG;
+  if (B > 0 && (!x || !w || !hist || !out)) return M2RNN_ERR_INVALID_ARG;
+  if (!dtypes_ok(io_dtype, M2RNN_F32) || !carry_grid_ok(B, 1, C)) return M2RNN_ERR_UNSUPPORTED;
+  if (B == 0) return M2RNN_OK;
+  CarryArgs a{};
+  a.B = B; a.T = 1; a.C = C; a.x = x; a.w = (const float*)w; a.bias = (const float*)bias;
+  a.hist_out = hist; a.out = out;
+  return status_of(launch_conv_carry(a, io_dtype, 2, (hipStream_t)stream));
+}
+
+// ---- group norm with a gate
+
+size_t m2rnn_groupnorm_workspace_bytes(int64_t rows, int64_t D, int64_t groups, int io_dtype) {
+  if (rows < 1 || D < 1 || groups < 1 || D % groups != 0 || !dtypes_ok(io_dtype, M2RNN_F32) ||
+      !groupnorm_grid_ok(rows, groups, D / groups, io_dtype))
+    return 0;
+  return align_up(groupnorm_workspace_floats(rows, groups, D / groups, io_dtype) * 4, 256);
+}
+
+int m2rnn_groupnorm_gate(int64_t rows, int64_t D, int64_t groups, int io_dtype, double eps,
+                         const void* y, const void* g_pre, const void* gamma, const void* beta,
+                         void* out, void* stream) {
+  if (rows < 0 || D < 1 || groups < 1 || D % groups != 0 || !(eps >= 0.0) || eps > 1e30 ||
+      !in_dtype_known(io_dtype))
+    return M2RNN_ERR_INVALID_ARG;
+  if (rows > 0 && (!y || !g_pre || !gamma || !beta || !out)) return M2RNN_ERR_INVALID_ARG;
+  if (!dtypes_ok(io_dtype, M2RNN_F32)) return M2RNN_ERR_UNSUPPORTED;
+  if (rows == 0) return M2RNN_OK;
+  if (!groupnorm_grid_ok(rows, groups, D / groups, io_dtype)) return M2RNN_ERR_UNSUPPORTED;
+  GroupNormArgs a{};
+  a.rows = rows; a.G = groups; a.S = D / groups; a.eps = (float)eps;
+  a.y = y; a.g_pre = g_pre; a.gamma = (const float*)gamma; a.beta = (const float*)beta;
+  a.out = out;
+  return status_of(launch_groupnorm_gate(a, io_dtype, false, (hipStream_t)stream));
+}
+
+int m2rnn_groupnorm_gate_bwd(int64_t rows, int64_t D, int64_t groups, int io_dtype, double eps,
+                             const void* y, const void* g_pre, const void* gamma,
+                             const void* beta, const void* dout, void* dy, void* dg_pre,
+                             void* dgamma, void* dbeta, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  if (rows < 0 || D < 1 || groups < 1 || D % groups != 0 || !(eps >= 0.0) || eps > 1e30 ||
+      !in_dtype_known(io_dtype))
+    return M2RNN_ERR_INVALID_ARG;
+  if (!dgamma || !dbeta) return M2RNN_ERR_INVALID_ARG;
+  if (rows > 0 && (!y || !g_pre || !gamma || !beta || !dout || !dy || !dg_pre))
+    return M2RNN_ERR_INVALID_ARG;
+  if (!dtypes_ok(io_dtype, M2RNN_F32)) return M2RNN_ERR_UNSUPPORTED;
+  const hipStream_t st = (hipStream_t)stream;
+  if (rows == 0) {  // sums over no rows
+    hipError_t e = fill(dgamma, nullptr, D, M2RNN_F32, st);
+    if (e == hipSuccess) e = fill(dbeta, nullptr, D, M2RNN_F32, st);
+    return status_of(e);
+  }
+  if (!groupnorm_grid_ok(rows, groups, D / groups, io_dtype)) return M2RNN_ERR_UNSUPPORTED;
+  const size_t need = m2rnn_groupnorm_workspace_bytes(rows, D, groups, io_dtype);
+  if (!workspace || workspace_bytes < need) return M2RNN_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return M2RNN_ERR_INVALID_ARG;
+  GroupNormArgs a{};
+  a.rows = rows; a.G = groups; a.S = D / groups; a.eps = (float)eps;
+  a.y = y; a.g_pre = g_pre; a.gamma = (const float*)gamma; a.beta = (const float*)beta;
+  a.dout = dout; a.dy = dy; a.dg_pre = dg_pre; a.dgamma = (float*)dgamma; a.dbeta = (float*)dbeta;
+  a.ws = (float*)workspace;
+  return status_of(launch_groupnorm_gate(a, io_dtype, true, st));
 }
 
 }  // extern "C"

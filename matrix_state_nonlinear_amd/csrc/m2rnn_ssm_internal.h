@@ -57,6 +57,22 @@ struct SsmContribArgs {
   int vb, vc;
 };
 
+// One token of every sequence.
+struct SsmStepArgs {
+  const void* k;        // [B, NQ, K]
+  const void* v;        // [B, N, V]
+  const void* q;        // [B, NQ, K]
+  const float* logit;   // [B, N]
+  const float* alpha;   // [N]
+  const float* beta;    // [N]
+  const float* w_r;     // [N, V]
+  float* H;             // [B, N, K, V], updated in place
+  void* y;              // [B, N, V]
+  int64_t B, N, NQ, K, V;
+  int lanes_v;          // lanes along V, set by the launcher
+};
+hipError_t launch_ssm_step(const SsmStepArgs& a, int in_dtype, hipStream_t stream);
+
 // Whole-call arguments (device pointers checked by the ABI).
 struct SsmArgs {
   const void* k;

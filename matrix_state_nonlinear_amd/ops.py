@@ -389,10 +389,48 @@ def m2rnn_gate_rmsnorm_bwd(y, g_pre, gamma, dout, eps: float = 1e-6, workspace=N
     return dy, dg, dgamma
 
 
+def _io_dtype(t, name):
+    """The dtype code of a tensor whose type sets a call's (float32 or bfloat16)."""
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    return _DT[t.dtype]
+
+
+def _call(name, dev, *args):
+    """Calls the library's function `name` on torch's current stream of the device `dev`, which
+    every tensor among the arguments must be on; raises what it returns."""
+    for t in args:
+        if isinstance(t, torch.Tensor) and t.device != dev:
+            raise ValueError(f"{name}: tensors on {t.device} and {dev}")
+    args = [_ptr(t) if isinstance(t, torch.Tensor) else t for t in args]
+    with torch.cuda.device(dev):  # the launches go to the stream's own device
+        st = getattr(_lib.lib(), name)(*args, _stream(dev))
+    check(st, name)
+
+
+def _given(spec, out, dev):
+    """Output buffers {name: (shape, dtype), or None for one that the call does not have}: those
+    given in ``out`` (None there skips dH0 and dhist), the others newly allocated."""
+    given = dict(out) if out is not None else {}
+    o = {}
+    for name, sd in spec.items():
+        if name in given:
+            o[name] = given[name]
+            if sd is None:
+                if o[name] is not None:
+                    raise ValueError(f"{name} is not an output of this call")
+            else:
+                (_opt if name in ("dH0", "dhist") else _need)(o[name], sd[0], sd[1], name)
+        else:
+            o[name] = None if sd is None else torch.empty(sd[0], dtype=sd[1], device=dev)
+    return o
+
+
 # ---- the selective state-space scan
 
 def _ssm_sizes(k, v, q, logit, alpha, beta, w_r, H0):
-    """Checks the scan's inputs; returns (B, T, N, NQ, K, V)."""
+    """Checks the scan's inputs; returns (B, T, N, NQ, K, V, dtype code)."""
+    io = _io_dtype(k, "k")
     N, NQ = _heads(k, v)
     B, T, _, K = k.shape
     V = v.shape[-1]
@@ -404,7 +442,7 @@ def _ssm_sizes(k, v, q, logit, alpha, beta, w_r, H0):
     _need(beta, (N,), f32, "beta")
     _need(w_r, (N, V), f32, "w_r")
     _opt(H0, (B, N, K, V), f32, "H0")
-    return B, T, N, NQ, K, V
+    return B, T, N, NQ, K, V, io
 
 
 def m2rnn_ssm_workspace_bytes(is_bwd: bool, B: int, T: int, n_heads: int, qk_heads: int, K: int,
@@ -422,7 +460,7 @@ def m2rnn_ssm_fwd(k, v, q, logit, alpha, beta, w_r, H0=None, want_ht: bool = Tru
     divides N as in m2rnn_fwd); logit [B, T, N], alpha, beta [N], w_r [N, V] and H0
     [B, N, K, V] float32.  Returns (y in v's dtype, HT float32 or None); ``out`` may hold
     preallocated (y, HT).  logit = -inf makes a token leave the state alone."""
-    B, T, N, NQ, K, V = _ssm_sizes(k, v, q, logit, alpha, beta, w_r, H0)
+    B, T, N, NQ, K, V, io = _ssm_sizes(k, v, q, logit, alpha, beta, w_r, H0)
     dev = k.device
     if out is not None:
         y, HT = out
@@ -433,10 +471,8 @@ def m2rnn_ssm_fwd(k, v, q, logit, alpha, beta, w_r, H0=None, want_ht: bool = Tru
     _opt(HT, (B, N, K, V), torch.float32, "HT")
     ws, wsb = _workspace(m2rnn_ssm_workspace_bytes(False, B, T, N, NQ, K, V, k.dtype), dev,
                          workspace)
-    st = _lib.lib().m2rnn_ssm_fwd(B, T, N, NQ, K, V, _DT[k.dtype], _ptr(k), _ptr(v), _ptr(q),
-                                  _ptr(logit), _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(H0),
-                                  _ptr(y), _ptr(HT), _ptr(ws), wsb, _stream(dev))
-    check(st, "m2rnn_ssm_fwd")
+    _call("m2rnn_ssm_fwd", dev, B, T, N, NQ, K, V, io, k, v, q, logit, alpha, beta, w_r, H0, y, HT,
+          ws, wsb)
     return y, HT
 
 
@@ -446,7 +482,7 @@ def m2rnn_ssm_bwd(k, v, q, logit, alpha, beta, w_r, H0, dy, dHT=None, want_dh0: 
     dbeta and dH0 (or None) in float32.  dy [B, T, N, V] in v's dtype, dHT [B, N, K, V] float32
     or None.  ``out`` may hold preallocated buffers under those names (any missing one is
     allocated; dH0 = None there skips it)."""
-    B, T, N, NQ, K, V = _ssm_sizes(k, v, q, logit, alpha, beta, w_r, H0)
+    B, T, N, NQ, K, V, io = _ssm_sizes(k, v, q, logit, alpha, beta, w_r, H0)
     f32 = torch.float32
     _need(dy, (B, T, N, V), v.dtype, "dy")
     _opt(dHT, (B, N, K, V), f32, "dHT")
@@ -455,24 +491,151 @@ def m2rnn_ssm_bwd(k, v, q, logit, alpha, beta, w_r, H0, dy, dHT=None, want_dh0: 
             "dq": ((B, T, NQ, K), k.dtype), "dlogit": ((B, T, N), f32), "dw_r": ((N, V), f32),
             "dalpha": ((N,), f32), "dbeta": ((N,), f32),
             "dH0": ((B, N, K, V), f32) if want_dh0 else None}
-    given = dict(out) if out is not None else {}
-    o = {}
-    for name, sd in spec.items():
-        if name in given:
-            o[name] = given[name]
-            if sd is None:
-                if o[name] is not None:
-                    raise ValueError("dH0 given with want_dh0=False")
-            else:
-                (_opt if name == "dH0" else _need)(o[name], sd[0], sd[1], name)
-        else:
-            o[name] = None if sd is None else torch.empty(sd[0], dtype=sd[1], device=dev)
+    o = _given(spec, out, dev)
     ws, wsb = _workspace(m2rnn_ssm_workspace_bytes(True, B, T, N, NQ, K, V, k.dtype), dev,
                          workspace)
-    st = _lib.lib().m2rnn_ssm_bwd(
-        B, T, N, NQ, K, V, _DT[k.dtype], _ptr(k), _ptr(v), _ptr(q), _ptr(logit), _ptr(alpha),
-        _ptr(beta), _ptr(w_r), _ptr(H0), _ptr(dy), _ptr(dHT), _ptr(o["dk"]), _ptr(o["dv"]),
-        _ptr(o["dq"]), _ptr(o["dlogit"]), _ptr(o["dw_r"]), _ptr(o["dalpha"]), _ptr(o["dbeta"]),
-        _ptr(o["dH0"]), _ptr(ws), wsb, _stream(dev))
-    check(st, "m2rnn_ssm_bwd")
+    _call("m2rnn_ssm_bwd", dev, B, T, N, NQ, K, V, io, k, v, q, logit, alpha, beta, w_r, H0, dy,
+          dHT, o["dk"], o["dv"], o["dq"], o["dlogit"], o["dw_r"], o["dalpha"], o["dbeta"], o["dH0"],
+          ws, wsb)
     return o
+
+
+def m2rnn_ssm_step(H, k, v, q, logit, alpha, beta, w_r, out=None):
+    """One token of every sequence through the scan (decoding): H [B, N, K, V] float32 is updated
+    in place from H_{t-1} to H_t, and y [B, N, V] in v's dtype is returned.  k, q [B, NQ, K] and v
+    [B, N, V] in float32 or bfloat16; logit [B, N], alpha, beta [N], w_r [N, V] float32."""
+    if H.dim() != 4 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("H must be [B, N, K, V], k and q [B, qk_heads, K], v [B, n_heads, V]")
+    B, N, K, V = H.shape
+    NQ = k.shape[1]
+    if (NQ < 1 or NQ > N or N % NQ) if N > 0 else NQ != 0:
+        raise ValueError(f"qk_heads = {NQ} must divide n_heads = {N}")
+    f32 = torch.float32
+    io = _io_dtype(k, "k")
+    _need(H, (B, N, K, V), f32, "H")
+    _need(k, (B, NQ, K), k.dtype, "k")
+    _need(q, (B, NQ, K), k.dtype, "q")
+    _need(v, (B, N, V), k.dtype, "v")
+    _need(logit, (B, N), f32, "logit")
+    _need(alpha, (N,), f32, "alpha")
+    _need(beta, (N,), f32, "beta")
+    _need(w_r, (N, V), f32, "w_r")
+    y = torch.empty((B, N, V), dtype=v.dtype, device=H.device) if out is None else out
+    _need(y, (B, N, V), v.dtype, "out")
+    _call("m2rnn_ssm_step", H.device, B, N, NQ, K, V, io, k, v, q, logit, alpha, beta, w_r, H, y)
+    return y
+
+
+# ---- the convolution with a carried history
+
+def m2rnn_conv_carry(x, w, bias=None, hist=None, want_hist: bool = True, lens=None, out=None):
+    """m2rnn_conv_silu with the three inputs before x: x [B, T, C] and hist [B, 3, C] (oldest
+    first, None = zero) in float32 or bfloat16, w [C, 4] and bias [C] float32.  Returns (out
+    [B, T, C], the history after x [B, 3, C] or None); ``lens`` [B] int32 says how many of each
+    sequence's inputs count for it (a padded batch).  ``out`` may hold preallocated (out, hist)."""
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, C]")
+    io = _io_dtype(x, "x")
+    B, T, C = x.shape
+    _need(w, (C, 4), torch.float32, "w")
+    _opt(bias, (C,), torch.float32, "bias")
+    _opt(hist, (B, 3, C), x.dtype, "hist")
+    _opt(lens, (B,), torch.int32, "lens")
+    if out is not None:
+        o, ho = out
+    else:
+        o = torch.empty_like(x)
+        ho = torch.empty((B, 3, C), dtype=x.dtype, device=x.device) if want_hist else None
+    _need(o, (B, T, C), x.dtype, "out")
+    _opt(ho, (B, 3, C), x.dtype, "hist_out")
+    if lens is not None and ho is None:
+        raise ValueError("lens sets the history that is returned: want_hist=False leaves it no use")
+    _call("m2rnn_conv_carry", x.device, B, T, C, io, x, w, bias, hist, lens, o, ho)
+    return o, ho
+
+
+def m2rnn_conv_carry_bwd(x, w, bias, hist, dout, workspace=None, out=None):
+    """Gradients of sum(dout * m2rnn_conv_carry(x, w, bias, hist)[0]): a dict with dx, dhist (x's
+    dtype; None without hist), dw and dbias (float32; None without bias).  dout in x's dtype;
+    ``out`` may hold preallocated buffers under those names."""
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, C]")
+    io = _io_dtype(x, "x")
+    B, T, C = x.shape
+    f32 = torch.float32
+    _need(w, (C, 4), f32, "w")
+    _opt(bias, (C,), f32, "bias")
+    _opt(hist, (B, 3, C), x.dtype, "hist")
+    _need(dout, (B, T, C), x.dtype, "dout")
+    spec = {"dx": ((B, T, C), x.dtype), "dw": ((C, 4), f32),
+            "dbias": ((C,), f32) if bias is not None else None,
+            "dhist": ((B, 3, C), x.dtype) if hist is not None else None}
+    o = _given(spec, out, x.device)
+    ws, wsb = _workspace(int(_lib.lib().m2rnn_conv_carry_workspace_bytes(B, T, C)), x.device,
+                         workspace)
+    _call("m2rnn_conv_carry_bwd", x.device, B, T, C, io, x, w, bias, hist, dout, o["dx"], o["dw"],
+          o["dbias"], o["dhist"], ws, wsb)
+    return o
+
+
+def m2rnn_conv_step(hist, x, w, bias=None, out=None):
+    """One token of every sequence through the convolution: hist [B, 3, C] is shifted by x
+    [B, C] in place, and SiLU of the convolution [B, C] is returned (all in x's dtype; w [C, 4]
+    and bias [C] float32)."""
+    if x.dim() != 2:
+        raise ValueError("x must be [B, C]")
+    io = _io_dtype(x, "x")
+    B, C = x.shape
+    _need(hist, (B, 3, C), x.dtype, "hist")
+    _need(w, (C, 4), torch.float32, "w")
+    _opt(bias, (C,), torch.float32, "bias")
+    o = torch.empty_like(x) if out is None else out
+    _need(o, (B, C), x.dtype, "out")
+    _call("m2rnn_conv_step", x.device, B, C, io, x, w, bias, hist, o)
+    return o
+
+
+# ---- group norm with a gate
+
+def _groupnorm_sizes(y, g_pre, gamma, beta, groups):
+    D = y.shape[-1]
+    if groups < 1 or D < 1 or D % groups:
+        raise ValueError(f"groups = {groups} must divide D = {D}")
+    _need(g_pre, tuple(y.shape), y.dtype, "g_pre")
+    _need(gamma, (D,), torch.float32, "gamma")
+    _need(beta, (D,), torch.float32, "beta")
+    return y.numel() // D, D, _io_dtype(y, "y")
+
+
+def m2rnn_groupnorm_gate(y, g_pre, gamma, beta, groups: int, eps: float = 1e-5, out=None):
+    """(gamma * z + beta) * SiLU(g_pre), z = y normalised (mean and variance) over each of the
+    ``groups`` runs of D / groups consecutive channels of the last dimension D.  y and g_pre
+    [..., D] in float32 or bfloat16, gamma and beta [D] float32; returns [..., D] in y's dtype."""
+    rows, D, io = _groupnorm_sizes(y, g_pre, gamma, beta, groups)
+    o = torch.empty_like(y) if out is None else out
+    _need(o, tuple(y.shape), y.dtype, "out")
+    _call("m2rnn_groupnorm_gate", y.device, rows, D, int(groups), io, float(eps), y, g_pre, gamma,
+          beta, o)
+    return o
+
+
+def m2rnn_groupnorm_gate_bwd(y, g_pre, gamma, beta, groups: int, dout, eps: float = 1e-5,
+                             workspace=None, out=None):
+    """Gradients of sum(dout * m2rnn_groupnorm_gate(...)): (dy, dg_pre) in y's dtype and (dgamma,
+    dbeta) in float32; ``out`` may hold those four preallocated."""
+    rows, D, io = _groupnorm_sizes(y, g_pre, gamma, beta, groups)
+    _need(dout, tuple(y.shape), y.dtype, "dout")
+    if out is not None:
+        dy, dg, dgamma, dbeta = out
+    else:
+        dy, dg = torch.empty_like(y), torch.empty_like(y)
+        dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(beta)
+    _need(dy, tuple(y.shape), y.dtype, "dy")
+    _need(dg, tuple(y.shape), y.dtype, "dg_pre")
+    _need(dgamma, (D,), torch.float32, "dgamma")
+    _need(dbeta, (D,), torch.float32, "dbeta")
+    nb = int(_lib.lib().m2rnn_groupnorm_workspace_bytes(rows, D, int(groups), io))
+    ws, wsb = _workspace(nb, y.device, workspace)
+    _call("m2rnn_groupnorm_gate_bwd", y.device, rows, D, int(groups), io, float(eps), y, g_pre,
+          gamma, beta, dout, dy, dg, dgamma, dbeta, ws, wsb)
+    return dy, dg, dgamma, dbeta

@@ -34,3 +34,9 @@ from .m2rnn_block import (  # noqa: F401
 )
 from .m2rnn_newton import newton_forward, newton_linearize  # noqa: F401
 from .m2rnn_ssm import ssm_backward, ssm_forward, ssm_step  # noqa: F401
+from .m2rnn_serving import (  # noqa: F401
+    conv_carry,
+    conv_carry_backward,
+    groupnorm_gate,
+    groupnorm_gate_backward,
+)
