@@ -17,7 +17,8 @@ SOURCES = ["m2rnn_api.hip", "m2rnn_gates.hip", "m2rnn_fwd.hip", "m2rnn_bwd.hip",
            "m2rnn_step.hip", "m2rnn_block.hip",
            "m2rnn_newton.hip", "m2rnn_ssm.hip", "m2rnn_ssm_bwd.hip",
            "m2rnn_ssm_step.hip", "m2rnn_carry.hip", "m2rnn_groupnorm.hip",
-           "m2rnn_ssm_sweep.hip", "m2rnn_ssm_sweep_f32.hip"]
+           "m2rnn_ssm_sweep.hip", "m2rnn_ssm_sweep_bf16_any.hip", "m2rnn_ssm_sweep_f32.hip",
+           "m2rnn_ssm_sweep_f32_any.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 VALU instructions are switched off for every kernel.  MFMA

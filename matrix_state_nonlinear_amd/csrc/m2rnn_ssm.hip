@@ -1,6 +1,9 @@
 // The selective state-space scan: segments of T, the pass between them, and the host side of
 // the forward (the sweep kernel itself is in m2rnn_ssm_sweep.h).
 //
+// A first kernel makes every token's step size and the running sums of its chunk's decays, which
+// all later passes read.
+//
 // A head's tokens can be split into segments that run at the same time: a first pass
 // computes what each segment adds to a zero state, a scan over the segments turns these into
 // every segment's starting state, and the sweep then runs all segments from theirs.  The
@@ -14,9 +17,12 @@ namespace {
 
 template <typename InT, int AT, int NT>
 hipError_t run(const SsmContribArgs& a, hipStream_t stream) {
-  const int64_t grid = a.B * a.N * a.nseg * a.slabs;
-  hipLaunchKernelGGL((ssm::m2rnn_ssm_contrib_kernel<InT, AT, NT>), dim3((unsigned)grid),
-                     dim3(256), 0, stream, a);
+  const dim3 grid((unsigned)(a.B * a.N * a.nseg * a.slabs));
+  const auto kernel = a.rev ? (a.vec ? ssm::m2rnn_ssm_contrib_kernel<InT, AT, NT, true, true>
+                                     : ssm::m2rnn_ssm_contrib_kernel<InT, AT, NT, true, false>)
+                            : (a.vec ? ssm::m2rnn_ssm_contrib_kernel<InT, AT, NT, false, true>
+                                     : ssm::m2rnn_ssm_contrib_kernel<InT, AT, NT, false, false>);
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 template <typename InT, int AT>
@@ -29,6 +35,42 @@ hipError_t pick_at(const SsmContribArgs& a, hipStream_t stream) {
   if (a.DA <= 64) return pick_nt<InT, 2>(a, stream);
   if (a.DA <= 128) return pick_nt<InT, 4>(a, stream);
   return pick_nt<InT, 8>(a, stream);
+}
+
+// Step sizes and chunk sums of log2 f for a workgroup's 64 tokens x 16 heads: logits come in
+// rows of heads and the results go out in rows of tokens, through LDS.  A wave sums four
+// heads, a lane per token; L = 32 has two chunks to a wave.
+template <int L>
+__global__ void __launch_bounds__(256)
+    m2rnn_ssm_decays_kernel(int64_t T, int64_t N, const float* __restrict__ logit,
+                            const float* __restrict__ alpha, const float* __restrict__ beta,
+                            double* __restrict__ cum, float* __restrict__ d) {
+  __shared__ float x[64][17];
+  const int64_t hb = (N + 15) / 16, tb = (T + 63) / 64;
+  const int64_t n0 = blockIdx.x % hb * 16, t0 = blockIdx.x / hb % tb * 64, b = blockIdx.x / hb / tb;
+  for (int i = threadIdx.x; i < 64 * 16; i += 256) {
+    const int64_t t = t0 + i / 16, n = n0 + i % 16;
+    x[i / 16][i % 16] = t < T && n < N ? logit[(b * T + t) * N + n] : 0.0f;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const int64_t n = n0 + 4 * w + h;
+    if (n >= N) return;
+    const float dt = ssm::softplus(x[lane][4 * w + h] + beta[n]);
+    double sum = t0 + lane < T ? ssm::log2_decay(alpha[n], dt) : 0.0;
+#pragma unroll
+    for (int s = 1; s < L; s *= 2) {
+      const double o = __shfl_up(sum, s);
+      if ((lane & (L - 1)) >= s) sum += o;
+    }
+    if (t0 + lane < T) {
+      const int64_t at = (b * N + n) * T + t0 + lane;
+      cum[at] = sum;
+      d[at] = dt;
+    }
+  }
 }
 
 // seg[u][s] (what segment s adds) -> the state at its start (rev: at its end, from later
@@ -81,7 +123,9 @@ SsmLayout ssm_fwd_layout(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V, 
   if (nseg > most) nseg = most;
   L.seglen = align_up((size_t)ceil_div(T > 0 ? T : 1, nseg), 64);
   L.nseg = ceil_div(T > 0 ? T : 1, L.seglen);
-  size_t off = 0;
+  size_t off = pad64((size_t)units * T * 2);  // cum, at 0
+  L.d = off;
+  off += pad64((size_t)units * T);
   if (L.nseg > 1) {
     L.hseg = off;
     off += pad64((size_t)units * L.nseg * K * V);
@@ -93,32 +137,46 @@ SsmLayout ssm_fwd_layout(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V, 
 }
 
 hipError_t launch_ssm_sweep(const SsmSweepArgs& a, int in_dtype, hipStream_t stream) {
-  return in_dtype == kBF16 ? launch_ssm_sweep_bf16(a, stream) : launch_ssm_sweep_f32(a, stream);
+  if (in_dtype == kBF16)
+    return a.vec ? launch_ssm_sweep_bf16(a, stream) : launch_ssm_sweep_bf16_any(a, stream);
+  return a.vec ? launch_ssm_sweep_f32(a, stream) : launch_ssm_sweep_f32_any(a, stream);
 }
 
-namespace {
-// Whether rows of `D` elements at p can be read in 16-byte pieces.
-int vec16(const void* p, int64_t D, int in_dtype) {
-  return aligned16(p) && D % (in_dtype == kBF16 ? 8 : 4) == 0;
+bool ssm_vec_rows(const void* p, int64_t heads, int64_t D, int elem_bytes) {
+  return aligned16(p) && D * elem_bytes % 16 == 0 && (double)heads * (double)D * elem_bytes < 16777216.0;
 }
-}  // namespace
+
+hipError_t launch_ssm_decays(const SsmArgs& a, int in_dtype, double* cum, float* d,
+                             hipStream_t stream) {
+  const dim3 grid((unsigned)(a.B * ceil_div(a.T, 64) * ceil_div(a.N, 16)));
+  if (in_dtype == kBF16)
+    hipLaunchKernelGGL(m2rnn_ssm_decays_kernel<ssm::Cfg<uint16_t>::L>, grid, dim3(256), 0, stream,
+                       a.T, a.N, a.logit, a.alpha, a.beta, cum, d);
+  else
+    hipLaunchKernelGGL(m2rnn_ssm_decays_kernel<ssm::Cfg<float>::L>, grid, dim3(256), 0, stream, a.T,
+                       a.N, a.logit, a.alpha, a.beta, cum, d);
+  return hipGetLastError();
+}
 
 hipError_t launch_ssm_fwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
   const SsmLayout L = ssm_fwd_layout(a.B, a.T, a.N, a.K, a.V, in_dtype);
-  const int grp = (int)(a.N / a.NQ);
+  const int grp = (int)(a.N / a.NQ), E = in_dtype == kBF16 ? 2 : 4;
   const float* start = a.H0;
-  hipError_t err;
+  double* cum = (double*)(a.ws + L.cum);
+  float* d = a.ws + L.d;
+  hipError_t err = launch_ssm_decays(a, in_dtype, cum, d, stream);
+  if (err != hipSuccess) return err;
+  const bool vk = ssm_vec_rows(a.k, a.NQ, a.K, E), vv = ssm_vec_rows(a.v, a.N, a.V, E);
   if (L.nseg > 1) {
     float* hseg = a.ws + L.hseg;
     float* fseg = a.ws + L.fseg;
     SsmContribArgs c{};
     c.b = a.k; c.c = a.v; c.b_grp = grp; c.c_grp = 1;
-    c.logit = a.logit; c.alpha = a.alpha; c.beta = a.beta;
+    c.cum = cum; c.d = d;
     c.contrib = hseg; c.fseg = fseg;
     c.B = a.B; c.T = a.T; c.N = a.N; c.nseg = L.nseg; c.seglen = L.seglen; c.slabs = 1;
     c.DA = (int)a.K; c.DC = (int)a.V; c.w_in = 1;
-    c.vb = vec16(a.k, a.K, in_dtype);
-    c.vc = vec16(a.v, a.V, in_dtype);
+    c.vec = vk && vv;
     if ((err = launch_ssm_contrib(c, in_dtype, stream)) != hipSuccess) return err;
     err = launch_ssm_segscan(hseg, fseg, a.H0, a.HT, a.B * a.N, L.nseg, a.K * a.V, false, stream);
     if (err != hipSuccess) return err;
@@ -127,18 +185,15 @@ hipError_t launch_ssm_fwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
   SsmSweepArgs s{};
   s.a = a.q; s.b = a.k; s.c = a.v;
   s.a_grp = grp; s.b_grp = grp; s.c_grp = 1; s.e_grp = 1;
-  s.logit = a.logit; s.alpha = a.alpha; s.beta = a.beta; s.skip = a.w_r;
+  s.cum = cum; s.d = d; s.skip = a.w_r;
   s.out = a.y;
   s.state0 = start;
   s.stateT = L.nseg > 1 ? nullptr : a.HT;
   s.B = a.B; s.T = a.T; s.N = a.N; s.nseg = L.nseg; s.seglen = L.seglen; s.slabs = 1;
   s.DA = (int)a.K; s.DC = (int)a.V;
   s.a_stride = (int)a.V; s.c_stride = 1;
-  s.w_in = 1;
-  s.va = vec16(a.q, a.K, in_dtype);
-  s.vb = vec16(a.k, a.K, in_dtype);
-  s.vc = vec16(a.v, a.V, in_dtype);
-  s.vo = a.V % 4 == 0 && aligned16(a.y);
+  s.mode = ssm::kY;
+  s.vec = vk && vv && ssm_vec_rows(a.q, a.NQ, a.K, E) && ssm_vec_rows(a.y, a.N, a.V, E);
   return launch_ssm_sweep(s, in_dtype, stream);
 }
 

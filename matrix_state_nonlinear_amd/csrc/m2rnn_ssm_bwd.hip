@@ -171,6 +171,8 @@ SsmLayout ssm_bwd_layout(int64_t B, int64_t T, int64_t N, int64_t NQ, int64_t K,
     return at;
   };
   const size_t KV = (size_t)K * V, U = (size_t)units;
+  L.cum = take(U * T * 2);
+  L.d = take(U * T);
   L.hseg = take(U * L.nseg * KV);
   L.gseg = take(U * L.nseg * KV);
   L.hT = take(U * KV);
@@ -194,31 +196,36 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
   const SsmLayout L = ssm_bwd_layout(a.B, a.T, a.N, a.NQ, a.K, a.V, in_dtype);
   const int grp = (int)(a.N / a.NQ);
   const int64_t units = a.B * a.N, KV = a.K * a.V;
-  const int epc = in_dtype == kBF16 ? 8 : 4;
-  auto vec = [&](const void* p, int64_t D) { return aligned16(p) && D % epc == 0 ? 1 : 0; };
-  auto vec4 = [&](const void* p, int64_t D) { return aligned16(p) && D % 4 == 0 ? 1 : 0; };
+  const int E = in_dtype == kBF16 ? 2 : 4;
+  const bool vk = ssm_vec_rows(a.k, a.NQ, a.K, E) && ssm_vec_rows(a.q, a.NQ, a.K, E),
+             vv = ssm_vec_rows(a.v, a.N, a.V, E) && ssm_vec_rows(a.dy, a.N, a.V, E), vec = vk && vv;
+  // the gradients' rows: of the input's type, or a shared head's fp32 parts
+  const bool vdv = ssm_vec_rows(a.dv, a.N, a.V, E),
+             vdq = grp > 1 ? ssm_vec_rows(a.ws, a.N, a.K, 4) : ssm_vec_rows(a.dq, a.N, a.K, E),
+             vdk = grp > 1 ? ssm_vec_rows(a.ws, a.N, a.K, 4) : ssm_vec_rows(a.dk, a.N, a.K, E);
+  double* cum = (double*)(a.ws + L.cum);
+  float* d = a.ws + L.d;
   float* hseg = a.ws + L.hseg;
   float* gseg = a.ws + L.gseg;
   float* fseg = a.ws + L.fseg;
   float* hT = a.ws + L.hT;
-  hipError_t err;
+  hipError_t err = launch_ssm_decays(a, in_dtype, cum, d, stream);
+  if (err != hipSuccess) return err;
 
   // the state at each segment's start, and the state gradient at its end; a single segment
   // starts from H0 and, without dHT, ends at zero
   const bool passes = L.nseg > 1 || a.dHT;
   if (passes) {
     SsmContribArgs c{};
-    c.logit = a.logit; c.alpha = a.alpha; c.beta = a.beta;
+    c.cum = cum; c.d = d; c.vec = vec;
     c.B = a.B; c.T = a.T; c.N = a.N; c.nseg = L.nseg; c.seglen = L.seglen;
     c.slabs = slabs_of(a.V);
     c.DA = (int)a.K; c.DC = (int)a.V;
     c.b = a.k; c.c = a.v; c.b_grp = grp; c.c_grp = 1;
     c.contrib = hseg; c.fseg = fseg; c.w_in = 1;
-    c.vb = vec(a.k, a.K); c.vc = vec(a.v, a.V);
     if ((err = launch_ssm_contrib(c, in_dtype, stream)) != hipSuccess) return err;
     c.b = a.q; c.c = a.dy;
     c.contrib = gseg; c.fseg = nullptr; c.w_in = 0; c.rev = 1;
-    c.vb = vec(a.q, a.K); c.vc = vec(a.dy, a.V);
     if ((err = launch_ssm_contrib(c, in_dtype, stream)) != hipSuccess) return err;
     err = launch_ssm_segscan(hseg, fseg, a.H0, hT, units, L.nseg, KV, false, stream);
     if (err != hipSuccess) return err;
@@ -227,7 +234,7 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
   }
 
   SsmSweepArgs s{};
-  s.logit = a.logit; s.alpha = a.alpha; s.beta = a.beta;
+  s.cum = cum; s.d = d;
   s.B = a.B; s.T = a.T; s.N = a.N; s.nseg = L.nseg; s.seglen = L.seglen;
 
   // dq: over dy and v, from the states
@@ -241,11 +248,10 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
   dq.pairs = a.ws + L.pairs;
   dq.colpairs = a.ws + L.colpairs;
   dq.colsum = a.ws + L.colsum;
-  dq.w_in = 1;
+  dq.mode = ssm::kDq;
   dq.out = grp > 1 ? (void*)(a.ws + L.dqp) : a.dq;
   dq.out_f32 = grp > 1;
-  dq.va = vec(a.dy, a.V); dq.vb = vec(a.v, a.V); dq.vc = vec(a.k, a.K);
-  dq.ve = vec(a.q, a.K); dq.vo = vec4(dq.out, a.K);
+  dq.vec = vec && vdq;
   if ((err = launch_ssm_sweep(dq, in_dtype, stream)) != hipSuccess) return err;
 
   // dv: over k and q in reverse, from the state gradients
@@ -262,9 +268,9 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
     dv.hend_last = hT;
   }
   dv.skip = a.w_r;
-  dv.rev = 1; dv.w_out = 1;
+  dv.mode = ssm::kDv;
   dv.out = a.dv;
-  dv.va = vec(a.k, a.K); dv.vb = vec(a.q, a.K); dv.vc = vec(a.dy, a.V); dv.vo = vec4(a.dv, a.V);
+  dv.vec = vec && vdv;
   if ((err = launch_ssm_sweep(dv, in_dtype, stream)) != hipSuccess) return err;
 
   // dk: over v and dy in reverse, from the transposed state gradients
@@ -275,11 +281,10 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
   dk.a_stride = 1; dk.c_stride = (int)a.V;
   dk.state0 = passes ? gseg : nullptr;
   dk.rowdot = a.ws + L.bdot;
-  dk.rev = 1; dk.w_out = 1;
+  dk.mode = ssm::kDk;
   dk.out = grp > 1 ? (void*)(a.ws + L.dkp) : a.dk;
   dk.out_f32 = grp > 1;
-  dk.va = vec(a.v, a.V); dk.vb = vec(a.dy, a.V); dk.vc = vec(a.q, a.K);
-  dk.ve = vec4(a.k, a.K); dk.vo = vec4(dk.out, a.K);
+  dk.vec = vec && vdk;
   if ((err = launch_ssm_sweep(dk, in_dtype, stream)) != hipSuccess) return err;
 
   hipLaunchKernelGGL(m2rnn_ssm_dgate_kernel, dim3((unsigned)ceil_div(units * L.nseg, 4)),

@@ -14,17 +14,16 @@ struct SsmSweepArgs {
   const void* a;        // [B, T, N / a_grp, DA]: head n reads head n / a_grp
   const void* b;        // [B, T, N / b_grp, DA]
   const void* c;        // [B, T, N / c_grp, DC]
-  const void* e;        // [B, T, N / e_grp, DC] or null: rowdot_p = e_p . (R_p S^T a_p)
-  const float* logit;   // [B, T, N]
-  const float* alpha;   // [N]
-  const float* beta;    // [N]
+  const void* e;        // [B, T, N / e_grp, DC] (dk, dq): rowdot_p = e_p . (R_p S^T a_p)
+  const double* cum;    // [B, N, T] sums of log2 f over each chunk (ssm_chunk tokens) up to a token
+  const float* d;       // [B, N, T] step sizes
   const float* skip;    // [N, DC] or null
   void* out;            // [B, T, N, DC], input type, or fp32 when out_f32
-  float* rowdot;        // [slabs, B, N, T] (e given)
-  float* pairs;         // [slabs, B, N, T] or null (e given): with M_ij = g_j D_ij (e_i . c_j)(a_i . b_j),
+  float* rowdot;        // [slabs, B, N, T] (dk, dq)
+  float* pairs;         // [slabs, B, N, T] (dq): with M_ij = g_j D_ij (e_i . c_j)(a_i . b_j),
                         // the sum of M over the chunk's pairs i >= p > j
-  float* colpairs;      // (pairs given) the sum of M_ip / g_p over the chunk's i >= p
-  float* colsum;        // [B, N, nseg, DA] or null: sum_p a_p (.) b_p
+  float* colpairs;      // (dq) the sum of M_ip / g_p over the chunk's i >= p
+  float* colsum;        // [B, N, nseg, DA] (dq): sum_p a_p (.) b_p
   const float* state0;  // [B, N, nseg, *] segment starts (or [B, N, *] when nseg = 1), or null = 0
   float* stateT;        // [B, N, *] or null: the state after the last token (nseg = 1 only)
   const float* hend;    // base only: [B, N, nseg, *], the other state at each segment's end is
@@ -35,26 +34,25 @@ struct SsmSweepArgs {
   int a_grp, b_grp, c_grp, e_grp;
   int DA, DC;
   int a_stride, c_stride;  // element strides of a state along DA and DC
-  int rev;                 // walk from the last token to the first
-  int w_in, w_out;         // the write strength d_p multiplies the inputs (g) / the outputs (rho)
+  int mode;                // which of the sweeps (kY .. kDq of m2rnn_ssm_sweep.h): the direction, and
+                           // whether d_p multiplies the inputs (g) or the outputs (rho)
   int out_f32;
-  int va, vb, vc, ve, vo;  // 16-byte (a, b, c) and 4-element (e, out) accesses allowed
+  int vec;                 // 16-byte accesses of a, b, c, e and 4-element ones of out allowed
 };
 
 // State that each segment of T adds to a zero start, and its decay.
 struct SsmContribArgs {
   const void* b;        // [B, T, N / b_grp, DA]
   const void* c;        // [B, T, N / c_grp, DC]
-  const float* logit;
-  const float* alpha;
-  const float* beta;
+  const double* cum;    // as above
+  const float* d;
   float* contrib;       // [B, N, nseg, DA, DC]
   float* fseg;          // [B, N, nseg] decay over a segment, or null
   int64_t B, T, N, nseg, seglen, slabs;
   int b_grp, c_grp;
   int DA, DC;
   int rev, w_in;
-  int vb, vc;
+  int vec;
 };
 
 // One token of every sequence.
@@ -103,6 +101,7 @@ struct SsmArgs {
 // into nseg segments of seglen tokens.
 struct SsmLayout {
   int64_t nseg, seglen;
+  size_t cum, d;                           // [B, N, T] double, float
   size_t hseg, fseg;                       // [B, N, nseg, K, V], [B, N, nseg] (nseg > 1 or backward)
   size_t gseg, hT, base, adot, bdot, pairs, colpairs;  // backward
   size_t colsum, gatepart, dqp, dkp;
@@ -114,11 +113,20 @@ SsmLayout ssm_bwd_layout(int64_t B, int64_t T, int64_t N, int64_t NQ, int64_t K,
 hipError_t launch_ssm_fwd(const SsmArgs& a, int in_dtype, hipStream_t stream);
 hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream);
 
-// The sweep's instances, one input type per file (they compile in parallel).
+// The sweep's instances, by input type, and by whether 16-byte accesses are allowed (not: _any),
+// each in a file of its own (they compile in parallel).
 hipError_t launch_ssm_sweep_bf16(const SsmSweepArgs& a, hipStream_t stream);
+hipError_t launch_ssm_sweep_bf16_any(const SsmSweepArgs& a, hipStream_t stream);
 hipError_t launch_ssm_sweep_f32(const SsmSweepArgs& a, hipStream_t stream);
+hipError_t launch_ssm_sweep_f32_any(const SsmSweepArgs& a, hipStream_t stream);
 hipError_t launch_ssm_sweep(const SsmSweepArgs& a, int in_dtype, hipStream_t stream);
 hipError_t launch_ssm_contrib(const SsmContribArgs& a, int in_dtype, hipStream_t stream);
+// The step sizes and, per chunk of the sweeps, the running sums of log2 f.
+hipError_t launch_ssm_decays(const SsmArgs& a, int in_dtype, double* cum, float* d,
+                             hipStream_t stream);
+// Whether rows of `heads` x `D` elements at p can be accessed in 16-byte pieces with 32-bit offsets
+// within a chunk.
+bool ssm_vec_rows(const void* p, int64_t heads, int64_t D, int elem_bytes);
 hipError_t launch_ssm_segscan(float* seg, const float* fseg, const float* first, float* last,
                               int64_t units, int64_t nseg, int64_t KV, bool rev,
                               hipStream_t stream);

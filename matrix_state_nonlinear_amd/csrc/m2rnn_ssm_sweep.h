@@ -160,29 +160,83 @@ __device__ __forceinline__ bf16x8 col8(const uint16_t* p, int stride, int m) {
   return __builtin_bit_cast(bf16x8, u32x4{xx[0], xx[1], yy[0], yy[1]});
 }
 
+// A workgroup barrier that orders LDS accesses only: global loads issued ahead and output
+// stores stay in flight across it (__syncthreads waits for them).
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+__device__ __forceinline__ int wave_index() {  // uniform
+  return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+}
+
 // ------------------------------------------------------------- staging
+// A [tokens, stride] array as a sweep walks it: `base` is at the current chunk's lowest token
+// (and the first column wanted), and row p of a chunk of `len` tokens in walking order is token p,
+// in reverse (REV) len - 1 - p.
+//
+// Accesses go through a buffer descriptor whose extent ends with the last row's columns: what lies
+// outside reads as zero and is not written, so no access needs a branch (a branch that
+// zeroes the register of a load in flight has to wait for it).  Offsets: kOut for columns that
+// do not exist; row p of a full chunk otherwise.  A short chunk walked in reverse shifts by the
+// missing rows, and rows that do not exist wrap below zero; a chunk has less than
+// 2^30 bytes (ssm_vec_rows), so neither can come back into the extent.
+template <int L, bool REV, bool VEC>
+struct Walk {
+  const char* base;                             // uniform
+  std::conditional_t<VEC, int, int64_t> stride; // bytes
+  int bytes;                                    // of a row, from base
+
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(int len) const {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (len - 1) * (int)stride + bytes,
+                                             0x00020000);
+  }
+  __device__ __forceinline__ uint32_t shift(int len) const {
+    return REV ? (uint32_t)((L - len) * (int)stride) : 0u;
+  }
+  __device__ __forceinline__ const char* row(int p, int len) const {
+    return base + (REV ? len - 1 - p : p) * (int64_t)stride;
+  }
+  __device__ __forceinline__ void next() { base += (REV ? -L : L) * (int64_t)stride; }
+};
+constexpr uint32_t kOut = 0x80000000u;
+
 // A tile of L rows (tokens) x W columns: 16-byte pieces, N of them per thread, fetched
 // into registers while the chunk before is worked on and written to LDS after it.
-template <typename InT, int W>
+template <typename InT, int W, bool REV, bool VEC>
 struct Tile {
-  static constexpr int L = Cfg<InT>::L, EPC = Cfg<InT>::epc, CPR = W / EPC,
+  using Rows = Walk<Cfg<InT>::L, REV, VEC>;
+  static constexpr int L = Cfg<InT>::L, EPC = Cfg<InT>::epc, CPR = W / EPC, RP = 256 / CPR,
                        N = L * CPR / 256, STRIDE = W + 8, PLANE = L * STRIDE;
-  static_assert(L * CPR % 256 == 0, "");
+  static_assert(L * CPR % 256 == 0 && 256 % CPR == 0, "");
   u32x4 r[N];
 
-  // rows p < len come from token first + step p; columns >= D and rows >= len are zero
-  __device__ __forceinline__ void fetch(const InT* base, int64_t row_stride, int64_t first, int step,
-                                        int len, int D, bool vec) {
+  // this thread's offset in a full chunk of rows of which D columns exist
+  static __device__ __forceinline__ uint32_t offset(const Rows& c, int D) {
+    const int row = (int)threadIdx.x / CPR, col = ((int)threadIdx.x % CPR) * EPC;
+    return col < D ? (uint32_t)((REV ? L - 1 - row : row) * (int)c.stride) +
+                         (uint32_t)(col * sizeof(InT))
+                   : kOut;
+  }
+  // rows p < len come from the chunk; columns >= D and rows >= len are zero
+  __device__ __forceinline__ void fetch(const Rows& c, uint32_t off, int len, int D) {
+    if constexpr (VEC) {
+      const auto rs = c.rsrc(len);
+      const uint32_t v = off - c.shift(len);
+      const uint32_t pass = (uint32_t)((REV ? -RP : RP) * c.stride);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int id = (int)threadIdx.x + 256 * i;
-      const int row = id / CPR, col = (id % CPR) * EPC;
-      u32x4 x{0, 0, 0, 0};
-      if (row < len && col < D) {
-        const InT* p = base + (first + (int64_t)step * row) * row_stride + col;
-        if (vec) {
-          x = *(const u32x4*)p;
-        } else {
+      for (int i = 0; i < N; ++i)
+        r[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(v + i * pass), 0, 0);
+    } else {
+      const int row0 = (int)threadIdx.x / CPR, col = ((int)threadIdx.x % CPR) * EPC;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int row = row0 + RP * i;
+        u32x4 x{0, 0, 0, 0};
+        if (row < len && col < D) {
+          const InT* p = (const InT*)c.row(row, len) + col;
 #pragma unroll
           for (int j = 0; j < EPC; ++j) {
             if (col + j < D) {
@@ -193,8 +247,8 @@ struct Tile {
             }
           }
         }
+        r[i] = x;
       }
-      r[i] = x;
     }
   }
   __device__ __forceinline__ void put(uint16_t* lds) const {
@@ -230,8 +284,8 @@ struct Tile {
 };
 
 // ------------------------------------------------------------- decays of a chunk
-// Per token p of the chunk, from the exact (double) prefix sums c_p: every power has an
-// exponent <= 0 and is rounded once.
+// Per token p of the chunk, from the exact (double) prefix sums c_p of log2 f: every power has
+// an exponent <= 0 and is rounded once.
 template <int L>
 struct Gates {
   float R[L];      // 2^{c_p}: from the carried state to p
@@ -257,56 +311,68 @@ __device__ __forceinline__ float softplus(float x) {
 __device__ __forceinline__ double log2_decay(float alpha, float d) {
   return fmax(-(double)alpha * (double)d * 1.4426950408889634, -2048.0);
 }
-__device__ __forceinline__ double shfl_d(double x, int lane) { return __shfl(x, lane); }
 
-// One wave: lane p has the logit of the chunk's token p (walking order) in x.  Going
-// forward the decay into p counts at p (inclusive sums); in reverse the decay between p
-// and p + 1 is p's own, so the sums are exclusive.
-template <int L>
-__device__ __forceinline__ void make_gates(Gates<L>& G, float x, float alpha, float beta, int len,
-                                           bool rev, bool w_in, bool w_out) {
-  const int lane = threadIdx.x & 63;
-  const float d = lane < len ? softplus(x + beta) : 0.0f;
-  const double l2 = lane < len ? log2_decay(alpha, d) : 0.0;
-  double inc = l2;
+// The prefix sums and step sizes of a chunk as one lane per token sees them, fetched a chunk ahead:
+// wave 0 makes R and the diagonal's parts from them, wave 1 W, wave 2 the tiles' input factors, wave
+// 3 the tiles' output factors.  Going forward the decay into p counts at p (the inclusive sums of
+// the chunk's tokens); in reverse the decay between p and p + 1 is p's own, which is the
+// chunk's total less the inclusive sum.
+template <int L, bool REV>
+struct GateRegs {
+  double c, total, end[3];  // end: the sums at the tiles' last tokens (wave 2: of the token's own tile)
+  float d;
+
+  // No branch and no scalar load: the loads stay in flight like the tiles' (kept in a wave's
+  // own branch, they would be waited for at its end).
+  __device__ __forceinline__ void fetch(const double* cum, const float* dt, int len) {
+    const int lane = threadIdx.x & 63, w = wave_index();
+    const auto rc = __builtin_amdgcn_make_buffer_rsrc((void*)cum, 0, len * 8, 0x00020000);
+    const auto rd = __builtin_amdgcn_make_buffer_rsrc((void*)dt, 0, len * 4, 0x00020000);
+    auto at = [&](int p) {
+      p = p < len ? p : len - 1;
+      return REV ? len - 1 - p : p;
+    };
+    auto sum = [&](int i) {
+      return __builtin_bit_cast(double, __builtin_amdgcn_raw_buffer_load_b64(rc, i * 8, 0, 0));
+    };
+    c = sum(at(lane));
+    total = sum(len - 1);
+    d = as_float(__builtin_amdgcn_raw_buffer_load_b32(rd, at(lane) * 4, 0, 0));
 #pragma unroll
-  for (int s = 1; s < 64; s *= 2) {
-    const double o = __shfl_up(inc, s);
-    if (lane >= s) inc += o;
+    for (int j = 0; j < L / 16 - 1; ++j) end[j] = sum(at(w == 2 ? lane | 15 : 16 * j + 15));
   }
-  const double total = shfl_d(inc, 63);
-  double prev = __shfl_up(inc, 1);
-  if (lane == 0) prev = 0.0;
-  const double c = rev ? prev : inc;
-  const double tile_end = shfl_d(c, lane | 15);
-  const float g = w_in ? d : 1.0f;
-  float rr[L / 16 - 1];
+  __device__ __forceinline__ void put(Gates<L>& G, bool w_in, bool w_out) const {
+    const int lane = threadIdx.x & 63, w = wave_index();
+    const double x = REV ? total - c : c;
+    const float g = w_in ? d : 1.0f;
+    if (lane < L) {
+      if (w == 0) {
+        G.R[lane] = pow2(x);
+        const float hi = (float)x;
+        G.chi[lane] = hi;
+        G.clo[lane] = (float)(x - (double)hi);
+        G.g[lane] = g;
+      } else if (w == 1) {
+        G.W[lane] = pow2(total - x) * g;
+        G.rho[lane] = w_out ? d : 1.0f;
+        if (lane == 0) G.total = pow2(total);
+      } else if (w == 2) {
+        const float et = pow2((REV ? total - end[0] : end[0]) - x);
+        G.et[lane] = et;
+        G.eg[lane] = et * g;
+      } else {
 #pragma unroll
-  for (int j = 0; j < L / 16 - 1; ++j) {
-    const double e = shfl_d(c, 16 * j + 15);
-    rr[j] = lane >= 16 * (j + 1) ? pow2(c - e) : 0.0f;
+        for (int j = 0; j < L / 16 - 1; ++j)
+          G.rr[j][lane] = lane >= 16 * (j + 1) ? pow2(x - (REV ? total - end[j] : end[j])) : 0.0f;
+      }
+    }
   }
-  if (lane < L) {
-    G.R[lane] = pow2(c);
-    G.W[lane] = pow2(total - c) * g;
-    const float et = pow2(tile_end - c);
-    G.et[lane] = et;
-    G.eg[lane] = et * g;
-#pragma unroll
-    for (int j = 0; j < L / 16 - 1; ++j) G.rr[j][lane] = rr[j];
-    const float hi = (float)c;
-    G.chi[lane] = hi;
-    G.clo[lane] = (float)(c - (double)hi);
-    G.g[lane] = g;
-    G.rho[lane] = w_out ? d : 1.0f;
-  }
-  if (lane == 0) G.total = pow2(total);
-}
+};
 
 // ------------------------------------------------------------- the sweep
-// What a sweep returns besides its output: nothing (y, dv); rowdot, the dot products of e with the
-// state's part of the output (dk: b / d); these (dq: a) and the sums over the pairs of a chunk.
-enum : int { kPlain = 0, kRowdot = 1, kPairs = 2 };
+// The four sweeps.  kDk also returns the dot products of e with the state's part of the output (b /
+// d), kDq these (a) and the sums over the pairs of a chunk.
+enum : int { kY = 0, kDv = 1, kDk = 2, kDq = 3 };
 
 // Sums over the pairs of a chunk, by 16 x 16 tile (it, jt) of M
 template <int L>
@@ -317,21 +383,22 @@ struct PairSums {
 };
 struct NoSums {};
 
-template <typename InT, int AT, int NT, int MODE>
+template <typename InT, int AT, int NT, int MODE, bool VEC>
 struct SweepShared {
   using C = Cfg<InT>;
   static constexpr int L = C::L;
-  using TA = Tile<InT, 32 * AT>;
-  using TC = Tile<InT, 64 * NT>;
+  static constexpr bool REV = MODE == kDv || MODE == kDk;
+  using TA = Tile<InT, 32 * AT, REV, VEC>;
+  using TC = Tile<InT, 64 * NT, REV, VEC>;
   static constexpr int PSTRIDE = L + 8;
   alignas(16) uint16_t a[C::planes * TA::PLANE];
   alignas(16) uint16_t b[C::planes * TA::PLANE];
   alignas(16) uint16_t c[C::planes * TC::PLANE];
-  alignas(16) uint16_t e[MODE == kPairs ? C::planes * TC::PLANE : 8];
+  alignas(16) uint16_t e[MODE == kDq ? C::planes * TC::PLANE : 8];
   alignas(16) uint16_t p[C::score_terms][L * PSTRIDE];
-  alignas(16) Gates<L> g[2];
+  alignas(16) Gates<L> g;
   alignas(16) float red[4][L];
-  std::conditional_t<MODE == kPairs, PairSums<L>, NoSums> sums;
+  std::conditional_t<MODE == kDq, PairSums<L>, NoSums> sums;
 };
 
 // Shifts within the 16-lane rows, zero beyond their ends: lane l reads lane l + N (l - N).
@@ -369,60 +436,98 @@ __device__ __forceinline__ float rows_sum(float x) {
   return x;
 }
 
-template <typename InT>
-__device__ __forceinline__ void store_cols4(void* out, int64_t i, f32x4 x, int left, bool vec,
-                                            bool f32) {
-  if (f32 || sizeof(InT) == 4) {
-    float* p = (float*)out + i;
-    if (vec) {
-      *(f32x4*)p = x;
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (r < left) p[r] = x[r];
-    }
-  } else {
-    uint16_t* p = (uint16_t*)out + i;
-    const u32x2 u{pack_rne(x[0], x[1]), pack_rne(x[2], x[3])};
-    if (vec) {
-      *(u32x2*)p = u;
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (r < left) p[r] = (uint16_t)(u[r / 2] >> (16 * (r & 1)));
-    }
-  }
+// Four consecutive columns of row p of a chunk: `off` as Tile::offset's for this lane's row and
+// columns, `it` 16-row tiles further on.  Without VEC: `left` of the columns exist.
+template <int L, bool REV, bool VEC>
+__device__ __forceinline__ int place4(const Walk<L, REV, VEC>& c, uint32_t off, int it, int len) {
+  const uint32_t tile = (uint32_t)((REV ? -16 : 16) * (int)c.stride) * (uint32_t)it;
+  return (int)(off - c.shift(len) + tile);
 }
-template <typename InT>
-__device__ __forceinline__ f32x4 load_cols4(const InT* p, int left, bool vec) {
-  f32x4 x{0, 0, 0, 0};
-  if (vec) {
-    if constexpr (sizeof(InT) == 2) {
-      const u32x2 u = *(const u32x2*)p;
-      x = f32x4{lo_half(u[0]), hi_half(u[0]), lo_half(u[1]), hi_half(u[1])};
-    } else {
-      x = *(const f32x4*)p;
-    }
+template <typename InT, int L, bool REV, bool VEC>
+__device__ __forceinline__ void store_cols4(const Walk<L, REV, VEC>& c, uint32_t off, int it, int p,
+                                            int len, f32x4 x, int col, int left, bool f32) {
+  if constexpr (VEC) {
+    const int v = place4(c, off, it, len);
+    if (f32 || sizeof(InT) == 4)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), c.rsrc(len), v, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_rne(x[0], x[1]), pack_rne(x[2], x[3])},
+                                            c.rsrc(len), v, 0, 0);
   } else {
+    if (p >= len) return;
+    char* row = (char*)c.row(p, len);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (r < left) x[r] = load_in(p + r);
+      if (r < left) {
+        if (f32 || sizeof(InT) == 4) ((float*)row)[col + r] = x[r];
+        else ((uint16_t*)row)[col + r] = (uint16_t)pack_rne(x[r], 0.0f);
+      }
+  }
+}
+// The same four columns of an input, as stored (widened when they are used: a value widened at once
+// would be waited for at once).
+template <typename InT, int L, bool REV, bool VEC>
+__device__ __forceinline__ u32x4 load_cols4(const Walk<L, REV, VEC>& c, uint32_t off, int it, int p,
+                                            int len, int col, int left) {
+  u32x4 x{0, 0, 0, 0};
+  if constexpr (VEC) {
+    const int v = place4(c, off, it, len);
+    if constexpr (sizeof(InT) == 2) {
+      const u32x2 u = __builtin_amdgcn_raw_buffer_load_b64(c.rsrc(len), v, 0, 0);
+      x[0] = u[0];
+      x[1] = u[1];
+    } else {
+      x = __builtin_amdgcn_raw_buffer_load_b128(c.rsrc(len), v, 0, 0);
+    }
+  } else if (p < len) {
+    const InT* row = (const InT*)c.row(p, len);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (r < left) {
+        if constexpr (sizeof(InT) == 2) x[r / 2] |= (uint32_t)row[col + r] << (16 * (r & 1));
+        else x[r] = bits(row[col + r]);
+      }
+  }
+  return x;
+}
+template <typename InT>
+__device__ __forceinline__ f32x4 widen4(u32x4 u) {
+  if constexpr (sizeof(InT) == 2)
+    return f32x4{lo_half(u[0]), hi_half(u[0]), lo_half(u[1]), hi_half(u[1])};
+  else
+    return __builtin_bit_cast(f32x4, u);
+}
+// sum of the terms of four consecutive columns in LDS
+template <int P>
+__device__ __forceinline__ f32x4 lds_cols4(const uint16_t* p, int plane) {
+  f32x4 x;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const u32x2 u = *(const u32x2*)(p + i * plane);
+    const f32x4 y{lo_half(u[0]), hi_half(u[0]), lo_half(u[1]), hi_half(u[1])};
+    x = i ? x + y : y;
   }
   return x;
 }
 
-template <typename InT, int AT, int NT, int MODE>
-__global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 1)
+// Workgroups per CU to allow registers for (LDS holds as many).
+constexpr int sweep_occupancy(int AT, int NT, int bytes) {
+  return bytes == 4 || AT * NT > 4 ? 1 : AT * NT > 2 ? 2 : 3;
+}
+
+template <typename InT, int AT, int NT, int MODE, bool VEC>
+__global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
     m2rnn_ssm_sweep_kernel(const SsmSweepArgs g) {
   using C = Cfg<InT>;
-  using S = SweepShared<InT, AT, NT, MODE>;
+  using S = SweepShared<InT, AT, NT, MODE, VEC>;
   using TA = typename S::TA;
   using TC = typename S::TC;
   constexpr int L = C::L, NI = L / 16, P = C::planes, PS = C::score_terms,
-                PH = MODE == kPlain ? C::state_terms : 3;
+                PH = MODE == kY || MODE == kDv ? C::state_terms : 3;
   __shared__ S sh;
 
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, m = lane & 15, q4 = lane >> 4;
+  const int lane = threadIdx.x & 63, m = lane & 15, q4 = lane >> 4;
+  const int w = wave_index();
   // workgroup id -> (b, segment, head, slab), slabs then heads fastest: the heads that
   // share q and k, and the slabs of a head, run on one XCD and share its L2
   int64_t u = xcd_remap((int)blockIdx.x, (int)gridDim.x);
@@ -434,31 +539,42 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
   const int64_t bi = u / g.nseg;
   const int64_t bn = bi * g.N + n;
   const int c0 = slab * 64 * NT;           // first column of this workgroup
-  const bool rev = g.rev != 0;
+  const int dc = g.DC - c0;                // columns left from c0
+  constexpr bool REV = S::REV, W_IN = MODE == kY || MODE == kDq, W_OUT = !W_IN;
+  constexpr int E = sizeof(InT);
 
   const int64_t seg0 = seg * g.seglen;
   const int64_t seg1 = seg0 + g.seglen < g.T ? seg0 + g.seglen : g.T;
   const int nch = (int)((seg1 - seg0 + L - 1) / L);
 
-  const int64_t ah = g.N / g.a_grp, bh = g.N / g.b_grp, ch_ = g.N / g.c_grp;
-  const InT* pa = (const InT*)g.a + (bi * g.T * ah + n / g.a_grp) * g.DA;
-  const InT* pb = (const InT*)g.b + (bi * g.T * bh + n / g.b_grp) * g.DA;
-  const InT* pc = (const InT*)g.c + (bi * g.T * ch_ + n / g.c_grp) * g.DC + c0;
-  const int64_t sa = ah * g.DA, sb = bh * g.DA, sc = ch_ * g.DC;
-  const float* pl = g.logit + bi * g.T * g.N + n;
-  const float alpha = g.alpha[n], beta = g.beta[n];
-  const int dc = g.DC - c0;                // columns left from c0
-
-  // the chunk i in walking order: first token, walking step and length
-  auto chunk_at = [&](int i) { return seg0 + (int64_t)(rev ? nch - 1 - i : i) * L; };
-  auto chunk_len = [&](int64_t t0) { return (int)(seg1 - t0 < L ? seg1 - t0 : L); };
-  const int step = rev ? -1 : 1;
-  auto first_tok = [&](int64_t t0, int len) { return rev ? t0 + len - 1 : t0; };
-  auto logit_of = [&](int i) {
-    const int64_t t0 = chunk_at(i);
-    const int len = chunk_len(t0);
-    return lane < len ? pl[(first_tok(t0, len) + step * lane) * g.N] : 0.0f;
+  // the first token of the chunk at hand and of the one being fetched
+  int64_t t0 = seg0 + (REV ? (int64_t)(nch - 1) * L : 0), tf = t0;
+  auto chunk_len = [&](int64_t t) { return (int)(seg1 - t < L ? seg1 - t : L); };
+  // an array of `D` columns of `e` bytes and N / grp heads, from column `col` of the first chunk
+  auto walk = [&](const void* p, int grp, int D, int col, int e) {
+    const int64_t heads = g.N / grp;
+    return Walk<L, REV, VEC>{(const char*)p + (((bi * g.T + t0) * heads + n / grp) * D + col) * e,
+                             (decltype(Walk<L, REV, VEC>::stride))(heads * D * e), (D - col) * e};
   };
+  const int oE = W_IN && MODE == kY ? E : g.out_f32 ? 4 : E;
+  auto ra = walk(g.a, g.a_grp, g.DA, 0, E), rb = walk(g.b, g.b_grp, g.DA, 0, E),
+       rc = walk(g.c, g.c_grp, g.DC, c0, E), ro = walk(g.out, 1, g.DC, c0, oE);
+  auto re = rc;
+  if constexpr (MODE == kDk || MODE == kDq) re = walk(g.e, g.e_grp, g.DC, c0, E);
+  const uint32_t oa = TA::offset(ra, g.DA), ob = TA::offset(rb, g.DA), oc = TC::offset(rc, dc),
+                 oe = MODE == kDq ? TC::offset(re, dc) : 0;
+  // this lane's place in the output and in e: row m of a 16-row tile, four columns of each of its
+  // wave's column tiles
+  uint32_t oo[NT], ox[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int col = 16 * (w * NT + nt) + 4 * q4, row = REV ? L - 1 - m : m;
+    oo[nt] = col < dc ? (uint32_t)(row * (int)ro.stride) + (uint32_t)(col * oE) : kOut;
+    ox[nt] = col < dc ? (uint32_t)(row * (int)re.stride) + (uint32_t)(col * E) : kOut;
+  }
+  const double* cum = g.cum + bn * g.T + t0;
+  const float* dts = g.d + bn * g.T + t0;
+  const int64_t tok0 = ((int64_t)slab * g.B * g.N + bn) * g.T;  // of the per-token results
 
   // scores above the diagonal stay zero: only tiles on and below it are ever written
   for (int i = threadIdx.x; i < (int)(sizeof(sh.p) / 16); i += 256) ((u32x4*)sh.p)[i] = u32x4{0, 0, 0, 0};
@@ -490,64 +606,85 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
       for (int s = 1; s < 64; s *= 2) dot += __shfl_xor(dot, s);
       double* red = (double*)&sh.red[0][0];
       if (lane == 0) red[w] = dot;
-      __syncthreads();
+      lds_barrier();
       if (threadIdx.x == 0)
         g.base[((int64_t)slab * g.B * g.N + bn) * g.nseg + seg] =
             (float)((red[0] + red[1]) + (red[2] + red[3]));
-      __syncthreads();
+      lds_barrier();
     }
   }
 
+  f32x4 skip[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int col = 16 * (w * NT + nt) + 4 * q4 + r;
+      skip[nt][r] = g.skip && col < dc ? g.skip[(int64_t)n * g.DC + c0 + col] : 0.0f;
+    }
+
   TA fa, fb;
   TC fc, fe;
-  const int64_t eh = g.N / g.e_grp;
-  const InT* pe = (const InT*)g.e + (bi * g.T * eh + n / g.e_grp) * g.DC + c0;
-  const int64_t se = eh * g.DC;
+  GateRegs<L, REV> fg;
+  u32x4 ev[MODE == kDk ? NI : 1][NT], ev_next[MODE == kDk ? NI : 1][NT];
   float csum[C::epc];
 #pragma unroll
   for (int j = 0; j < C::epc; ++j) csum[j] = 0.0f;
-  const bool do_col = g.colsum != nullptr && slab == 0;
-
-  float xl = 0.0f;  // wave 3: the logits of the next chunk whose gates it makes
-  {
-    const int64_t t0 = chunk_at(0);
-    const int len = chunk_len(t0);
-    fa.fetch(pa, sa, first_tok(t0, len), step, len, g.DA, g.va);
-    fb.fetch(pb, sb, first_tok(t0, len), step, len, g.DA, g.vb);
-    fc.fetch(pc, sc, first_tok(t0, len), step, len, dc, g.vc);
-    if constexpr (MODE == kPairs) fe.fetch(pe, se, first_tok(t0, len), step, len, dc, g.ve);
-    if (w == 3) {
-      const float x = logit_of(0);
-      if (nch > 1) xl = logit_of(1);
-      make_gates<L>(sh.g[0], x, alpha, beta, len, rev, g.w_in, g.w_out);
+  const bool do_col = MODE == kDq && slab == 0;
+  auto fetch = [&]() {  // the chunk at tf, and on to the next
+    const int len = chunk_len(tf);
+    fa.fetch(ra, oa, len, g.DA);
+    fb.fetch(rb, ob, len, g.DA);
+    fc.fetch(rc, oc, len, dc);
+    if constexpr (MODE == kDq) fe.fetch(re, oe, len, dc);
+    if constexpr (MODE == kDk) {
+#pragma unroll
+      for (int it = 0; it < NI; ++it)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int cc = 16 * (w * NT + nt) + 4 * q4;
+          ev_next[it][nt] = load_cols4<InT>(re, ox[nt], it, 16 * it + m, len, cc, dc - cc);
+        }
+    }
+    fg.fetch(cum, dts, len);
+    ra.next();
+    rb.next();
+    rc.next();
+    if constexpr (MODE == kDk || MODE == kDq) re.next();
+    cum += REV ? -L : L;
+    dts += REV ? -L : L;
+    tf += REV ? -L : L;
+  };
+  auto put = [&]() {
+    if constexpr (MODE == kDk) {
+#pragma unroll
+      for (int it = 0; it < NI; ++it)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) ev[it][nt] = ev_next[it][nt];
     }
     fa.put(sh.a);
     fb.put(sh.b);
     fc.put(sh.c);
-    if constexpr (MODE == kPairs) fe.put(sh.e);
-    if (do_col) TA::dot_cols(fa, fb, csum);
-  }
-  __syncthreads();
+    if constexpr (MODE == kDq) {
+      fe.put(sh.e);
+      if (do_col) TA::dot_cols(fa, fb, csum);
+    }
+    fg.put(sh.g, W_IN, W_OUT);
+  };
+  fetch();
+  put();
+  lds_barrier();
 
   for (int ch = 0; ch < nch; ++ch) {
-    const int64_t t0 = chunk_at(ch);
     const int len = chunk_len(t0);
-    const Gates<L>& G = sh.g[ch & 1];
-    if (ch + 1 < nch) {
-      const int64_t t1 = chunk_at(ch + 1);
-      const int len1 = chunk_len(t1);
-      fa.fetch(pa, sa, first_tok(t1, len1), step, len1, g.DA, g.va);
-      fb.fetch(pb, sb, first_tok(t1, len1), step, len1, g.DA, g.vb);
-      fc.fetch(pc, sc, first_tok(t1, len1), step, len1, dc, g.vc);
-      if constexpr (MODE == kPairs) fe.fetch(pe, se, first_tok(t1, len1), step, len1, dc, g.ve);
-    }
+    const Gates<L>& G = sh.g;
+    if (ch + 1 < nch) fetch();
 
-    // scores: tile (it, jt), jt <= it, of a b^T, decayed and split.  Waves 0..2 take every
-    // third tile; wave 3 the last one of ten and the next chunk's gates.
+    // scores: tile (it, jt), jt <= it, of a b^T, decayed and split; a wave takes every fourth
     constexpr int TILES = NI * (NI + 1) / 2;
 #pragma unroll
-    for (int rd = 0; rd < (TILES > 9 ? 3 : (TILES + 2) / 3); ++rd) {
-      const int idx = w < 3 ? rd * 3 + w : (rd == 0 && TILES > 9 ? 9 : TILES);
+    for (int rd = 0; rd < (TILES + 3) / 4; ++rd) {
+      const int idx = rd * 4 + w;
       if (idx < TILES) {
         const int it = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0;
         const int jt = idx - it * (it + 1) / 2;
@@ -577,13 +714,13 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
             s[r] = j0 + r <= i ? s[r] * dec : 0.0f;
           }
         } else {
-          const f32x4 e4 = *(const f32x4*)((MODE == kPairs ? G.et : G.eg) + j0);
-          if constexpr (MODE == kPairs) g4 = *(const f32x4*)(G.g + j0);
+          const f32x4 e4 = *(const f32x4*)((MODE == kDq ? G.et : G.eg) + j0);
+          if constexpr (MODE == kDq) g4 = *(const f32x4*)(G.g + j0);
           const float ri = G.rr[jt][i];
 #pragma unroll
           for (int r = 0; r < 4; ++r) s[r] *= ri * e4[r];
         }
-        if constexpr (MODE == kPairs) {
+        if constexpr (MODE == kDq) {
           // the other factor of M: c . e (k . q)
           f32x4 qk{0, 0, 0, 0};
           const uint16_t* re = sh.e + (16 * it + m) * TC::STRIDE + 8 * q4;
@@ -617,7 +754,7 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
             if (q4 == 0) sh.sums.rs[jt][i] = sum;
           }
         }
-        if (MODE == kPairs || it == jt) s *= g4;
+        if (MODE == kDq || it == jt) s *= g4;
         uint32_t x0[PS], x1[PS];
         split2<PS>(s[0], s[1], x0);
         split2<PS>(s[2], s[3], x1);
@@ -626,12 +763,6 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
           *(u32x2*)(sh.p[p] + i * S::PSTRIDE + j0) = u32x2{x0[p], x1[p]};
       }
     }
-    if (w == 3 && ch + 1 < nch) {
-      make_gates<L>(sh.g[(ch + 1) & 1], xl, alpha, beta, chunk_len(chunk_at(ch + 1)), rev, g.w_in,
-                    g.w_out);
-      if (ch + 2 < nch) xl = logit_of(ch + 2);
-    }
-
     // readout of the carried state: lane holds out[i = 16 it + m][c = 4 q4 + r]
     f32x4 acc[NI][NT];
 #pragma unroll
@@ -663,7 +794,7 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) acc[it][nt] *= R;
     }
-    if constexpr (MODE != kPlain) {
+    if constexpr ((MODE == kDk || MODE == kDq)) {
       // e . (the state's part of the output), this wave's columns
 #pragma unroll
       for (int it = 0; it < NI; ++it) {
@@ -671,33 +802,26 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
         float dot = 0.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int cc = 16 * (w * NT + nt) + 4 * q4, left = dc - cc;
-          f32x4 ev{0, 0, 0, 0};
-          if constexpr (MODE == kPairs) {
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-              const u32x2 uu = *(const u32x2*)(sh.e + p * TC::PLANE + i * TC::STRIDE + cc);
-              ev += f32x4{lo_half(uu[0]), hi_half(uu[0]), lo_half(uu[1]), hi_half(uu[1])};
-            }
-          } else if (i < len && left > 0) {
-            ev = load_cols4(pe + (first_tok(t0, len) + step * i) * se + cc, left, g.ve);
-          }
+          const int cc = 16 * (w * NT + nt) + 4 * q4;
+          f32x4 y;
+          if constexpr (MODE == kDq) y = lds_cols4<P>(sh.e + i * TC::STRIDE + cc, TC::PLANE);
+          else y = widen4<InT>(ev[it][nt]);
           const f32x4 x = acc[it][nt];
-          dot += (ev[0] * x[0] + ev[1] * x[1]) + (ev[2] * x[2] + ev[3] * x[3]);
+          dot += (y[0] * x[0] + y[1] * x[1]) + (y[2] * x[2] + y[3] * x[3]);
         }
         dot = rows_sum(dot);
         if (q4 == 0) sh.red[w][i] = dot;
       }
     }
-    __syncthreads();  // the scores are in LDS
+    lds_barrier();  // the scores are in LDS
 
-    if constexpr (MODE != kPlain) {
+    if constexpr ((MODE == kDk || MODE == kDq)) {
       if (w == 2 && lane < len) {
-        const int64_t o = ((int64_t)slab * g.B * g.N + bn) * g.T + first_tok(t0, len) + step * lane;
+        const int64_t o = tok0 + t0 + (REV ? len - 1 - lane : lane);
         g.rowdot[o] = (sh.red[0][lane] + sh.red[1][lane]) + (sh.red[2][lane] + sh.red[3][lane]);
       }
     }
-    if constexpr (MODE == kPairs) {
+    if constexpr (MODE == kDq) {
       if (w == 3) {
         // per token t: all pairs i >= t > j of the chunk, from the tiles' sums; and sum_i M_it / d_t
         const int t = lane & (L - 1), tt = t >> 4;
@@ -717,7 +841,7 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
           x += tt == 1 ? s20 + s30 : tt == 2 ? s30 + s31 : 0.0f;
         }
         if (lane < len) {
-          const int64_t o = ((int64_t)slab * g.B * g.N + bn) * g.T + first_tok(t0, len) + step * lane;
+          const int64_t o = tok0 + t0 + (REV ? len - 1 - lane : lane);
           g.pairs[o] = x;
           g.colpairs[o] = coltot + sh.sums.cs[tt][t];
         }
@@ -771,39 +895,22 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
 #pragma unroll
     for (int it = 0; it < NI; ++it) {
       const int i = 16 * it + m;
-      const bool ok = i < len;
-      const int64_t tok = first_tok(t0, len) + step * i;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int cc = 16 * (w * NT + nt) + 4 * q4;
         f32x4 x = acc[it][nt];
-        const int left = dc - cc;
-        x *= G.rho[i];
-        if (g.skip && left > 0) {
-          f32x4 cv{0, 0, 0, 0};
-#pragma unroll
-          for (int p = 0; p < P; ++p) {
-            const u32x2 uu = *(const u32x2*)(sh.c + p * TC::PLANE + i * TC::STRIDE + cc);
-            cv += f32x4{lo_half(uu[0]), hi_half(uu[0]), lo_half(uu[1]), hi_half(uu[1])};
-          }
-          const float* ps = g.skip + (int64_t)n * g.DC + c0 + cc;
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (r < left) x[r] += ps[r] * cv[r];
-        }
-        if (ok && left > 0)
-          store_cols4<InT>(g.out, ((bi * g.T + tok) * g.N + n) * g.DC + c0 + cc, x, left, g.vo,
-                           g.out_f32);
+        if constexpr (W_OUT) x *= G.rho[i];
+        if constexpr (MODE == kY || MODE == kDv)
+          x += skip[nt] * lds_cols4<P>(sh.c + i * TC::STRIDE + cc, TC::PLANE);
+        store_cols4<InT>(ro, oo[nt], it, i, len, x, cc, dc - cc, oE > E);
       }
     }
-    __syncthreads();  // everybody is done with the tiles
+    ro.next();
+    t0 += REV ? -L : L;
+    lds_barrier();  // everybody is done with the tiles
     if (ch + 1 < nch) {
-      fa.put(sh.a);
-      fb.put(sh.b);
-      fc.put(sh.c);
-      if constexpr (MODE == kPairs) fe.put(sh.e);
-      if (do_col) TA::dot_cols(fa, fb, csum);
-      __syncthreads();
+      put();
+      lds_barrier();
     }
   }
 
@@ -821,11 +928,11 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
         }
   }
   if (do_col) {  // threads with the same columns: 256 / CPR of them, summed in order
-    __syncthreads();
+    lds_barrier();
     float* red = (float*)sh.a;
 #pragma unroll
     for (int j = 0; j < C::epc; ++j) red[threadIdx.x * C::epc + j] = csum[j];
-    __syncthreads();
+    lds_barrier();
     for (int col = threadIdx.x; col < g.DA; col += 256) {
       float sum = 0.0f;
       for (int k = col / C::epc; k < 256; k += TA::CPR) sum += red[k * C::epc + col % C::epc];
@@ -835,20 +942,21 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
 }
 
 // The state a segment adds to a zero start: the sweep's state update alone.
-template <typename InT, int AT, int NT>
+template <typename InT, int AT, int NT, bool REV, bool VEC>
 __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 1)
     m2rnn_ssm_contrib_kernel(const SsmContribArgs g) {
   using C = Cfg<InT>;
-  using TB = Tile<InT, 32 * AT>;
-  using TC = Tile<InT, 64 * NT>;
-  constexpr int L = C::L, P = C::planes;
+  using TB = Tile<InT, 32 * AT, REV, VEC>;
+  using TC = Tile<InT, 64 * NT, REV, VEC>;
+  constexpr int L = C::L, P = C::planes, E = sizeof(InT);
   struct Sh {
     alignas(16) uint16_t b[P * TB::PLANE];
     alignas(16) uint16_t c[P * TC::PLANE];
-    alignas(16) Gates<L> g[2];
+    alignas(16) Gates<L> g;
   };
   __shared__ Sh sh;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, m = lane & 15, q4 = lane >> 4;
+  const int lane = threadIdx.x & 63, m = lane & 15, q4 = lane >> 4;
+  const int w = wave_index();
   int64_t u = xcd_remap((int)blockIdx.x, (int)gridDim.x);
   const int slab = (int)(u % g.slabs);
   u /= g.slabs;
@@ -858,26 +966,20 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
   const int64_t bi = u / g.nseg;
   const int64_t bn = bi * g.N + n;
   const int c0 = slab * 64 * NT;
-  const bool rev = g.rev != 0;
   const int64_t seg0 = seg * g.seglen;
   const int64_t seg1 = seg0 + g.seglen < g.T ? seg0 + g.seglen : g.T;
   const int nch = (int)((seg1 - seg0 + L - 1) / L);
-  const int64_t bh = g.N / g.b_grp, ch_ = g.N / g.c_grp;
-  const InT* pb = (const InT*)g.b + (bi * g.T * bh + n / g.b_grp) * g.DA;
-  const InT* pc = (const InT*)g.c + (bi * g.T * ch_ + n / g.c_grp) * g.DC + c0;
-  const int64_t sb = bh * g.DA, sc = ch_ * g.DC;
-  const float* pl = g.logit + bi * g.T * g.N + n;
-  const float alpha = g.alpha[n], beta = g.beta[n];
   const int dc = g.DC - c0;
-  auto chunk_at = [&](int i) { return seg0 + (int64_t)(rev ? nch - 1 - i : i) * L; };
-  auto chunk_len = [&](int64_t t0) { return (int)(seg1 - t0 < L ? seg1 - t0 : L); };
-  const int step = rev ? -1 : 1;
-  auto first_tok = [&](int64_t t0, int len) { return rev ? t0 + len - 1 : t0; };
-  auto logit_of = [&](int i) {
-    const int64_t t0 = chunk_at(i);
-    const int len = chunk_len(t0);
-    return lane < len ? pl[(first_tok(t0, len) + step * lane) * g.N] : 0.0f;
+  int64_t tf = seg0 + (REV ? (int64_t)(nch - 1) * L : 0);
+  auto walk = [&](const void* p, int grp, int D, int col) {
+    const int64_t heads = g.N / grp;
+    return Walk<L, REV, VEC>{(const char*)p + (((bi * g.T + tf) * heads + n / grp) * D + col) * E,
+                             (decltype(Walk<L, REV, VEC>::stride))(heads * D * E), (D - col) * E};
   };
+  auto rb = walk(g.b, g.b_grp, g.DA, 0), rc = walk(g.c, g.c_grp, g.DC, c0);
+  const uint32_t ob = TB::offset(rb, g.DA), oc = TC::offset(rc, dc);
+  const double* cum = g.cum + bn * g.T + tf;
+  const float* dts = g.d + bn * g.T + tf;
 
   f32x4 st[2 * AT][NT];
 #pragma unroll
@@ -887,33 +989,29 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
   float ftot = 1.0f;
   TB fb;
   TC fc;
-  float xl = 0.0f;
-  {
-    const int64_t t0 = chunk_at(0);
-    const int len = chunk_len(t0);
-    fb.fetch(pb, sb, first_tok(t0, len), step, len, g.DA, g.vb);
-    fc.fetch(pc, sc, first_tok(t0, len), step, len, dc, g.vc);
-    if (w == 3) {
-      const float x = logit_of(0);
-      if (nch > 1) xl = logit_of(1);
-      make_gates<L>(sh.g[0], x, alpha, beta, len, rev, g.w_in, false);
-    }
+  GateRegs<L, REV> fg;
+  auto fetch = [&]() {
+    const int len = (int)(seg1 - tf < L ? seg1 - tf : L);
+    fb.fetch(rb, ob, len, g.DA);
+    fc.fetch(rc, oc, len, dc);
+    fg.fetch(cum, dts, len);
+    rb.next();
+    rc.next();
+    cum += REV ? -L : L;
+    dts += REV ? -L : L;
+    tf += REV ? -L : L;
+  };
+  auto put = [&]() {
     fb.put(sh.b);
     fc.put(sh.c);
-  }
-  __syncthreads();
+    fg.put(sh.g, g.w_in, false);
+  };
+  fetch();
+  put();
+  lds_barrier();
   for (int ch = 0; ch < nch; ++ch) {
-    const Gates<L>& G = sh.g[ch & 1];
-    if (ch + 1 < nch) {
-      const int64_t t1 = chunk_at(ch + 1);
-      const int len1 = chunk_len(t1);
-      fb.fetch(pb, sb, first_tok(t1, len1), step, len1, g.DA, g.vb);
-      fc.fetch(pc, sc, first_tok(t1, len1), step, len1, dc, g.vc);
-      if (w == 3) {
-        make_gates<L>(sh.g[(ch + 1) & 1], xl, alpha, beta, len1, rev, g.w_in, false);
-        if (ch + 2 < nch) xl = logit_of(ch + 2);
-      }
-    }
+    const Gates<L>& G = sh.g;
+    if (ch + 1 < nch) fetch();
     const float f = G.total;
     ftot *= f;
 #pragma unroll
@@ -948,11 +1046,10 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
         for (int nt = 0; nt < NT; ++nt) st[at][nt] = mfma_terms(xb, cw[nt], st[at][nt]);
       }
     }
-    __syncthreads();
+    lds_barrier();
     if (ch + 1 < nch) {
-      fb.put(sh.b);
-      fc.put(sh.c);
-      __syncthreads();
+      put();
+      lds_barrier();
     }
   }
   float* o = g.contrib + (bn * g.nseg + seg) * (int64_t)g.DA * g.DC;
