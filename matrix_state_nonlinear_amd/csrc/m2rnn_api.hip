@@ -138,13 +138,13 @@ bool newton_supported(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
 }
 
 // The state-space scan's shapes: the recurrence's, and grids of fewer than 2^32 threads in
-// the backward (segments x heads, two 128-column slabs at most, and one thread for each element of a
+// the backward (segments x heads, four slabs of columns at most, and one thread for each element of a
 // shared head's gradient).
 bool ssm_supported(int64_t B, int64_t T, int64_t N, int64_t NQ, int64_t K, int64_t V) {
   if (!sizes_supported(B, T, N, K, V)) return false;
   if (B * T * N == 0) return true;
   const SsmLayout L = ssm_bwd_layout(B, T, N, NQ, K, V, M2RNN_F32);
-  return 2.0 * (double)B * (double)N * (double)L.nseg < (double)(1 << 24) &&
+  return 4.0 * (double)B * (double)N * (double)L.nseg < (double)(1 << 24) &&
          (double)B * (double)T * (double)NQ * (double)K < 4294967296.0 &&
          (double)B * (double)N * (double)K * (double)V < 4294967296.0;
 }

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(256) m2rnn_conv_carry_kernel(const CarryArgs g
 template <typename IoT, int VEC>
 __global__ void __launch_bounds__(256)
     m2rnn_conv_carry_bwd_kernel(const CarryArgs g, int64_t runs, float* __restrict__ part) {
-  __shared__ float red[kRunsPerGroup][5][64 * VEC];
+  __shared__ float red[kRunsPerGroup][64 * VEC];
   const int64_t Cv = g.C / VEC, cblocks = (Cv + 63) / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t grp = blockIdx.x / cblocks;
@@ -161,17 +161,16 @@ __global__ void __launch_bounds__(256)
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < 5; ++i)
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) red[wave][i][lane * VEC + k] = s[i][k];
-  __syncthreads();
   const int64_t c0 = blockIdx.x % cblocks * 64 * VEC;
-  for (int i = threadIdx.x; i < 5 * 64 * VEC; i += 256) {
-    const int col = i % (64 * VEC), k = i / (64 * VEC);
-    if (c0 + col < g.C)
-      part[(grp * 5 + k) * g.C + c0 + col] =
-          (red[0][k][col] + red[1][k][col]) + (red[2][k][col] + red[3][k][col]);
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    if (i) __syncthreads();
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) red[wave][lane * VEC + k] = s[i][k];
+    __syncthreads();
+    for (int col = threadIdx.x; col < 64 * VEC; col += 256)
+      if (c0 + col < g.C)
+        part[(grp * 5 + i) * g.C + c0 + col] = (red[0][col] + red[1][col]) + (red[2][col] + red[3][col]);
   }
 }
 

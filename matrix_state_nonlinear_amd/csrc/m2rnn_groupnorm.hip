@@ -107,18 +107,20 @@ __global__ void __launch_bounds__(256) m2rnn_groupnorm_gate_kernel(const GroupNo
 // With a = gamma z + beta, da = dout SiLU(g_pre), dz = da gamma:
 //     dy = rs (dz - mean(dz) - z mean(dz z)),  dg_pre = dout a SiLU'(g_pre),
 //     dgamma = sum_rows da z,  dbeta = sum_rows da.
+// The four waves of a workgroup take the same columns of four neighbouring row blocks.
 template <typename IoT, int VEC, int NCH>
 __global__ void __launch_bounds__(256) m2rnn_groupnorm_gate_bwd_kernel(const GroupNormArgs g) {
-  const int64_t wid = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  __shared__ float red[4][2][64 * VEC * NCH];
+  const int wave = threadIdx.x >> 6;
   const int64_t cblocks = (g.G + g.gw - 1) / g.gw;
   const Place p(g);
-  const int64_t grp = wid % cblocks * g.gw + p.grp, rb = wid / cblocks;
+  const int64_t grp = blockIdx.x % cblocks * g.gw + p.grp, quad = blockIdx.x / cblocks;
+  const int64_t rb = quad * 4 + wave;
   const int rp = 64 / (g.lg * g.gw);
   const int64_t r0 = rb * g.rows_per;
   const int64_t r1 = r0 + g.rows_per < g.rows ? r0 + g.rows_per : g.rows;
   const int S = (int)g.S;
-  if (r0 >= g.rows) return;  // whole waves
-  const bool live = grp < g.G;
+  const bool live = grp < g.G;  // (a wave behind the last row has nothing to add)
   const float inv = 1.0f / (float)S;
   Piece<float, VEC, NCH> gam, bet;
   if (live) {
@@ -177,21 +179,29 @@ __global__ void __launch_bounds__(256) m2rnn_groupnorm_gate_bwd_kernel(const Gro
       }
     }
   }
-  // join the pass's rows, then one partial per row block: part[rb][2][D]
+  // join the pass's rows, then the four waves: one partial per workgroup, part[quad][2][D]
+  const int lanes = g.lg * g.gw;  // that hold different columns
 #pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int j = (c * g.lg + p.l) * VEC;
+  for (int c = 0; c < NCH; ++c)
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      for (int s = g.lg * g.gw; s < 64; s *= 2) {
+      for (int s = lanes; s < 64; s *= 2) {
         sg[c][k] += __shfl_xor(sg[c][k], s);
         sb[c][k] += __shfl_xor(sb[c][k], s);
       }
-      if (live && p.row == 0 && j < S) {
-        float* o = g.ws + rb * 2 * g.G * S + grp * S + j + k;
-        o[0] = sg[c][k];
-        o[g.G * S] = sb[c][k];
-      }
+      const int i = ((threadIdx.x & 63) * NCH + c) * VEC + k;
+      red[wave][0][i] = sg[c][k];
+      red[wave][1][i] = sb[c][k];
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < lanes * NCH * VEC; i += 256) {
+    const int lane = i / (NCH * VEC), c = i / VEC % NCH, k = i % VEC;
+    const int64_t gr = blockIdx.x % cblocks * g.gw + lane / g.lg;
+    const int j = (c * g.lg + lane % g.lg) * VEC + k;
+    if (gr < g.G && j < S) {
+      float* o = g.ws + quad * 2 * g.G * S + gr * S + j;
+      o[0] = (red[0][0][i] + red[1][0][i]) + (red[2][0][i] + red[3][0][i]);
+      o[g.G * S] = (red[0][1][i] + red[1][1][i]) + (red[2][1][i] + red[3][1][i]);
     }
   }
 }
@@ -295,9 +305,10 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 struct Plan {
   int lg, gw, nch;
   int64_t rows_per, blocks;  // rows per wave (per workgroup when too wide), row blocks
+  int64_t parts;             // partials of the backward
 };
 Plan plan(int64_t rows, int64_t G, int64_t S, int vec, bool bwd) {
-  Plan p{1, 1, 0, 1, 1};
+  Plan p{1, 1, 0, 1, 1, 1};
   const int64_t pieces = ceil_div(S, vec);
   while (p.lg < 64 && p.lg < pieces) p.lg *= 2;
   const int64_t nch = ceil_div(pieces, p.lg);
@@ -317,16 +328,19 @@ Plan plan(int64_t rows, int64_t G, int64_t S, int vec, bool bwd) {
   per = per < 1 ? 1 : per > most ? most : per;
   p.rows_per = per * rp;
   p.blocks = ceil_div(rows, p.rows_per);
+  p.parts = p.nch ? ceil_div(p.blocks, 4) : p.blocks;
   return p;
 }
 
 template <typename IoT, int VEC, int NCH>
 hipError_t run(const GroupNormArgs& g, bool bwd, int64_t blocks, hipStream_t stream) {
-  const dim3 grid((unsigned)ceil_div(blocks * ceil_div(g.G, g.gw), 4));
+  const int64_t cblocks = ceil_div(g.G, g.gw);
   if (bwd)
-    hipLaunchKernelGGL((m2rnn_groupnorm_gate_bwd_kernel<IoT, VEC, NCH>), grid, dim3(256), 0, stream, g);
+    hipLaunchKernelGGL((m2rnn_groupnorm_gate_bwd_kernel<IoT, VEC, NCH>),
+                       dim3((unsigned)(ceil_div(blocks, 4) * cblocks)), dim3(256), 0, stream, g);
   else
-    hipLaunchKernelGGL((m2rnn_groupnorm_gate_kernel<IoT, VEC, NCH>), grid, dim3(256), 0, stream, g);
+    hipLaunchKernelGGL((m2rnn_groupnorm_gate_kernel<IoT, VEC, NCH>),
+                       dim3((unsigned)ceil_div(blocks * cblocks, 4)), dim3(256), 0, stream, g);
   return hipGetLastError();
 }
 template <typename IoT, int VEC>
@@ -349,7 +363,7 @@ hipError_t pick(GroupNormArgs g, bool bwd, hipStream_t stream) {
   }
   if (e != hipSuccess || !bwd) return e;
   hipLaunchKernelGGL(m2rnn_groupnorm_sum_kernel, dim3((unsigned)ceil_div(2 * g.G * g.S, 64)),
-                     dim3(1024), 0, stream, p.blocks, g.G * g.S, g.ws, g.dgamma, g.dbeta);
+                     dim3(1024), 0, stream, p.parts, g.G * g.S, g.ws, g.dgamma, g.dbeta);
   return hipGetLastError();
 }
 template <typename IoT>
@@ -366,8 +380,8 @@ hipError_t pick(const GroupNormArgs& g, bool bwd, hipStream_t stream) {
 // not known here).
 size_t groupnorm_workspace_floats(int64_t rows, int64_t G, int64_t S, int io_dtype) {
   const int vec = io_dtype == kBF16 ? io::kVec<uint16_t> : io::kVec<float>;
-  const int64_t a = plan(rows, G, S, 1, true).blocks;
-  const int64_t b = S % vec == 0 ? plan(rows, G, S, vec, true).blocks : 0;
+  const int64_t a = plan(rows, G, S, 1, true).parts;
+  const int64_t b = S % vec == 0 ? plan(rows, G, S, vec, true).parts : 0;
   return (size_t)(a > b ? a : b) * 2 * (size_t)(G * S);
 }
 
@@ -376,7 +390,7 @@ bool groupnorm_grid_ok(int64_t rows, int64_t G, int64_t S, int io_dtype) {
   for (int v : {1, vec})
     for (bool bwd : {false, true}) {
       const Plan p = plan(rows, G, S, v, bwd);
-      const double wgs = p.nch ? (double)p.blocks * (double)ceil_div(G, p.gw) / 4.0 + 1.0
+      const double wgs = p.nch ? ((double)p.blocks / 4.0 + 1.0) * (double)ceil_div(G, p.gw)
                                : (double)p.blocks * (double)G;
       if (wgs >= (double)(1 << 24)) return false;
     }

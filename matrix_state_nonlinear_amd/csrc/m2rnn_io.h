@@ -86,11 +86,9 @@ __device__ __forceinline__ void store(uint16_t* p, const Vals<N>& v) {
 template <typename IoT>
 constexpr int kVec = 16 / (int)sizeof(IoT);
 
+// 1 / (1 + e^-x): the exponential runs to infinity or zero at the ends and its reciprocal to 0 or 1.
 __device__ __forceinline__ float sigmoid(float x) {
-  // exp(-|x|) never overflows
-  const float e = __expf(-fabsf(x));
-  const float r = __frcp_rn(1.0f + e);
-  return x >= 0.0f ? r : e * r;
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));
 }
 
 }  // namespace io

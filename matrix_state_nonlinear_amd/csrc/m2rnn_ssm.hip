@@ -15,19 +15,24 @@ namespace m2rnn {
 
 namespace {
 
-template <typename InT, int AT, int NT>
+template <typename InT, int AT, int NT, int RS>
 hipError_t run(const SsmContribArgs& a, hipStream_t stream) {
   const dim3 grid((unsigned)(a.B * a.N * a.nseg * a.slabs));
-  const auto kernel = a.rev ? (a.vec ? ssm::m2rnn_ssm_contrib_kernel<InT, AT, NT, true, true>
-                                     : ssm::m2rnn_ssm_contrib_kernel<InT, AT, NT, true, false>)
-                            : (a.vec ? ssm::m2rnn_ssm_contrib_kernel<InT, AT, NT, false, true>
-                                     : ssm::m2rnn_ssm_contrib_kernel<InT, AT, NT, false, false>);
+  const auto kernel = a.rev ? (a.vec ? ssm::m2rnn_ssm_contrib_kernel<InT, AT, NT, RS, true, true>
+                                     : ssm::m2rnn_ssm_contrib_kernel<InT, AT, NT, RS, true, false>)
+                            : (a.vec ? ssm::m2rnn_ssm_contrib_kernel<InT, AT, NT, RS, false, true>
+                                     : ssm::m2rnn_ssm_contrib_kernel<InT, AT, NT, RS, false, false>);
   hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 template <typename InT, int AT>
 hipError_t pick_nt(const SsmContribArgs& a, hipStream_t stream) {
-  return a.DC <= 64 ? run<InT, AT, 1>(a, stream) : run<InT, AT, 2>(a, stream);
+  if constexpr (AT <= 2)
+    if (ssm_columns(a.DA, a.DC) == 128) return run<InT, AT, 2, 1>(a, stream);
+  if constexpr (AT > 1)  // a wave keeps at least one 16-row tile of the state
+    if (a.DC <= 16) return run<InT, AT, 1, 4>(a, stream);
+  if (a.DC <= 32) return run<InT, AT, 1, 2>(a, stream);
+  return run<InT, AT, 1, 1>(a, stream);
 }
 template <typename InT>
 hipError_t pick_at(const SsmContribArgs& a, hipStream_t stream) {
@@ -113,13 +118,18 @@ hipError_t launch_ssm_segscan(float* seg, const float* fseg, const float* first,
   return hipGetLastError();
 }
 
-// Segments of the forward: as many as bring the grid to two workgroups per CU, of at
-// least 128 tokens.
+// Workgroups of the forward's sweep that a CU holds (m2rnn_ssm_sweep.h).
+int64_t ssm_per_cu(int64_t K, int64_t V, int in_dtype) {
+  return in_dtype == kBF16 && K <= 64 && V <= 64 ? 3 : 2;
+}
+
+// Segments of the forward: as many as fill every CU once, of at least 64 tokens.
 SsmLayout ssm_fwd_layout(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V, int in_dtype) {
   SsmLayout L{};
-  const int64_t units = B * N;
-  int64_t nseg = units > 0 ? ceil_div(512, units) : 1;
-  const int64_t most = T / 128 > 1 ? T / 128 : 1;
+  const int64_t units = B * N, wgs = units * ssm_slabs(K, V);
+  const int64_t want = 256 * ssm_per_cu(K, V, in_dtype);
+  int64_t nseg = wgs > 0 ? ceil_div(want, wgs) : 1;
+  const int64_t most = T / 64 > 1 ? T / 64 : 1;
   if (nseg > most) nseg = most;
   L.seglen = align_up((size_t)ceil_div(T > 0 ? T : 1, nseg), 64);
   L.nseg = ceil_div(T > 0 ? T : 1, L.seglen);
@@ -174,7 +184,8 @@ hipError_t launch_ssm_fwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
     c.b = a.k; c.c = a.v; c.b_grp = grp; c.c_grp = 1;
     c.cum = cum; c.d = d;
     c.contrib = hseg; c.fseg = fseg;
-    c.B = a.B; c.T = a.T; c.N = a.N; c.nseg = L.nseg; c.seglen = L.seglen; c.slabs = 1;
+    c.B = a.B; c.T = a.T; c.N = a.N; c.nseg = L.nseg; c.seglen = L.seglen;
+    c.slabs = ssm_slabs(a.K, a.V);
     c.DA = (int)a.K; c.DC = (int)a.V; c.w_in = 1;
     c.vec = vk && vv;
     if ((err = launch_ssm_contrib(c, in_dtype, stream)) != hipSuccess) return err;
@@ -189,7 +200,8 @@ hipError_t launch_ssm_fwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
   s.out = a.y;
   s.state0 = start;
   s.stateT = L.nseg > 1 ? nullptr : a.HT;
-  s.B = a.B; s.T = a.T; s.N = a.N; s.nseg = L.nseg; s.seglen = L.seglen; s.slabs = 1;
+  s.B = a.B; s.T = a.T; s.N = a.N; s.nseg = L.nseg; s.seglen = L.seglen;
+  s.slabs = ssm_slabs(a.K, a.V);
   s.DA = (int)a.K; s.DC = (int)a.V;
   s.a_stride = (int)a.V; s.c_stride = 1;
   s.mode = ssm::kY;

@@ -23,7 +23,6 @@ constexpr double kNoPass = 15.0;  // -log of 3e-7
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t pad64(size_t x) { return align_up(x, 64); }
-int64_t slabs_of(int64_t DC) { return DC <= 64 ? 1 : ceil_div(DC, 128); }
 
 // One wave per (b, n, segment), from its last chunk to its first (chunks of `L` tokens, as
 // in the sweeps).
@@ -177,11 +176,11 @@ SsmLayout ssm_bwd_layout(int64_t B, int64_t T, int64_t N, int64_t NQ, int64_t K,
   L.gseg = take(U * L.nseg * KV);
   L.hT = take(U * KV);
   L.fseg = take(U * L.nseg);
-  L.base = take(U * L.nseg * slabs_of(V));
-  L.adot = take(U * T * slabs_of(K));
-  L.bdot = take(U * T * slabs_of(K));
-  L.pairs = take(U * T * slabs_of(K));
-  L.colpairs = take(U * T * slabs_of(K));
+  L.base = take(U * L.nseg * ssm_slabs(K, V));
+  L.adot = take(U * T * ssm_slabs(V, K));
+  L.bdot = take(U * T * ssm_slabs(V, K));
+  L.pairs = take(U * T * ssm_slabs(V, K));
+  L.colpairs = take(U * T * ssm_slabs(V, K));
   L.colsum = take(U * L.nseg * V);
   L.gatepart = take(U * L.nseg * 2);
   if (NQ < N) {
@@ -219,7 +218,7 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
     SsmContribArgs c{};
     c.cum = cum; c.d = d; c.vec = vec;
     c.B = a.B; c.T = a.T; c.N = a.N; c.nseg = L.nseg; c.seglen = L.seglen;
-    c.slabs = slabs_of(a.V);
+    c.slabs = ssm_slabs(a.K, a.V);
     c.DA = (int)a.K; c.DC = (int)a.V;
     c.b = a.k; c.c = a.v; c.b_grp = grp; c.c_grp = 1;
     c.contrib = hseg; c.fseg = fseg; c.w_in = 1;
@@ -241,7 +240,7 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
   SsmSweepArgs dq = s;
   dq.a = a.dy; dq.b = a.v; dq.c = a.k; dq.e = a.q;
   dq.a_grp = 1; dq.b_grp = 1; dq.c_grp = grp; dq.e_grp = grp;
-  dq.DA = (int)a.V; dq.DC = (int)a.K; dq.slabs = slabs_of(a.K);
+  dq.DA = (int)a.V; dq.DC = (int)a.K; dq.slabs = ssm_slabs(a.V, a.K);
   dq.a_stride = 1; dq.c_stride = (int)a.V;
   dq.state0 = passes ? hseg : a.H0;
   dq.rowdot = a.ws + L.adot;
@@ -258,7 +257,7 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
   SsmSweepArgs dv = s;
   dv.a = a.k; dv.b = a.q; dv.c = a.dy;
   dv.a_grp = grp; dv.b_grp = grp; dv.c_grp = 1; dv.e_grp = 1;
-  dv.DA = (int)a.K; dv.DC = (int)a.V; dv.slabs = slabs_of(a.V);
+  dv.DA = (int)a.K; dv.DC = (int)a.V; dv.slabs = ssm_slabs(a.K, a.V);
   dv.a_stride = (int)a.V; dv.c_stride = 1;
   dv.state0 = passes ? gseg : nullptr;
   dv.stateT = passes ? nullptr : a.dH0;
@@ -277,7 +276,7 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
   SsmSweepArgs dk = s;
   dk.a = a.v; dk.b = a.dy; dk.c = a.q; dk.e = a.k;
   dk.a_grp = 1; dk.b_grp = 1; dk.c_grp = grp; dk.e_grp = grp;
-  dk.DA = (int)a.V; dk.DC = (int)a.K; dk.slabs = slabs_of(a.K);
+  dk.DA = (int)a.V; dk.DC = (int)a.K; dk.slabs = ssm_slabs(a.V, a.K);
   dk.a_stride = 1; dk.c_stride = (int)a.V;
   dk.state0 = passes ? gseg : nullptr;
   dk.rowdot = a.ws + L.bdot;
@@ -290,7 +289,7 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
   hipLaunchKernelGGL(m2rnn_ssm_dgate_kernel, dim3((unsigned)ceil_div(units * L.nseg, 4)),
                      dim3(256), 0, stream, a.B, a.T, a.N, L.nseg, L.seglen,
                      in_dtype == kBF16 ? ssm::Cfg<uint16_t>::L : ssm::Cfg<float>::L,
-                     (int)slabs_of(a.K), (int)slabs_of(a.V), a.ws + L.adot, a.ws + L.bdot,
+                     (int)ssm_slabs(a.V, a.K), (int)ssm_slabs(a.K, a.V), a.ws + L.adot, a.ws + L.bdot,
                      a.ws + L.pairs, a.ws + L.colpairs, passes ? a.ws + L.base : nullptr, a.logit,
                      a.alpha, a.beta, a.dlogit, a.ws + L.gatepart);
   if ((err = hipGetLastError()) != hipSuccess) return err;

@@ -97,6 +97,15 @@ struct SsmArgs {
   int64_t B, T, N, NQ, K, V;
 };
 
+// Columns of the output (DC of the sweep, contracting over DA) per workgroup: up to 128, or 64
+// where a 128-column state would not leave registers for two workgroups per CU (one prompt of
+// 16384 tokens, 32 heads, K = V = 128: 230 us with 128 columns, SLABUS us with 64).
+inline int ssm_columns(int64_t DA, int64_t DC) { return DC > 64 && DA <= 64 ? 128 : 64; }
+inline int64_t ssm_slabs(int64_t DA, int64_t DC) {
+  const int c = ssm_columns(DA, DC);
+  return (DC + c - 1) / c;
+}
+
 // Workspace of a call: offsets in floats (64-float aligned) and the split of T
 // into nseg segments of seglen tokens.
 struct SsmLayout {

@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(256) m2rnn_ssm_step_kernel(const SsmStepArgs g
       v[c][j] = col < V ? load_in(vp + col) : 0.0f;
       acc[c][j] = 0.0f;
     }
-  constexpr int U = 8;
+  constexpr int U = 4;
   for (int r = r0; r < K; r += rows * W * U) {
     io::Vals<VEC> h[U][NB];
     float kd[U], q[U];
@@ -133,7 +133,7 @@ hipError_t run(SsmStepArgs g, bool vec, hipStream_t stream) {
 
 hipError_t launch_ssm_step(const SsmStepArgs& g, int in_dtype, hipStream_t stream) {
   const bool vec = g.V % 4 == 0 && aligned16(g.H);
-  // a wave holds 8 x 64 x 4 elements in flight: larger heads are shared by four waves, and so are
+  // a wave holds 4 x 64 x 4 elements in flight: larger heads are shared by four waves, and so are
   // the heads of calls that would leave most CUs without a wave
   const bool split = g.K * g.V > 4096 || (g.B * g.N < 512 && g.K * g.V >= 1024);
   if (in_dtype == kBF16)

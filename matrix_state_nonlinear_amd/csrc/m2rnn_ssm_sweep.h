@@ -22,7 +22,8 @@
 // decay does not cost precision.
 //
 // A workgroup (4 waves) walks one segment of one head, the state in MFMA
-// accumulators throughout: wave w owns 16 NT columns of it, all DA rows.  All
+// accumulators throughout: a wave owns 16 NT columns of it, all DA rows.  Where there are fewer
+// than 64 columns, RS waves own the same ones and share the chunk's output rows.  All
 // products use the 16x16x32 bf16 MFMA (16 times the rate of the fp32 one); bf16
 // inputs are exact operands, and every fp32 operand (the decayed scores, the state,
 // the decayed inputs of the state update, and fp32 inputs) is split into bf16
@@ -172,6 +173,13 @@ __device__ __forceinline__ int wave_index() {  // uniform
   return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
 }
 
+// The same value, but unknown to the compiler to be it: addresses formed from it are not kept in
+// registers across the sweep's other phases.
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // ------------------------------------------------------------- staging
 // A [tokens, stride] array as a sweep walks it: `base` is at the current chunk's lowest token
 // (and the first column wanted), and row p of a chunk of `len` tokens in walking order is token p,
@@ -209,14 +217,14 @@ template <typename InT, int W, bool REV, bool VEC>
 struct Tile {
   using Rows = Walk<Cfg<InT>::L, REV, VEC>;
   static constexpr int L = Cfg<InT>::L, EPC = Cfg<InT>::epc, CPR = W / EPC, RP = 256 / CPR,
-                       N = L * CPR / 256, STRIDE = W + 8, PLANE = L * STRIDE;
-  static_assert(L * CPR % 256 == 0 && 256 % CPR == 0, "");
+                       N = (L * CPR + 255) / 256, STRIDE = W + 8, PLANE = L * STRIDE;
+  static_assert((L * CPR % 256 == 0 || L * CPR < 256) && 256 % CPR == 0, "");
   u32x4 r[N];
 
   // this thread's offset in a full chunk of rows of which D columns exist
   static __device__ __forceinline__ uint32_t offset(const Rows& c, int D) {
     const int row = (int)threadIdx.x / CPR, col = ((int)threadIdx.x % CPR) * EPC;
-    return col < D ? (uint32_t)((REV ? L - 1 - row : row) * (int)c.stride) +
+    return col < D && row < L ? (uint32_t)((REV ? L - 1 - row : row) * (int)c.stride) +
                          (uint32_t)(col * sizeof(InT))
                    : kOut;
   }
@@ -255,6 +263,7 @@ struct Tile {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int id = (int)threadIdx.x + 256 * i;
+      if (L * CPR < 256 && id >= L * CPR) break;
       uint16_t* p = lds + (id / CPR) * STRIDE + (id % CPR) * EPC;
       if constexpr (EPC == 8) {
         *(u32x4*)p = r[i];
@@ -383,13 +392,13 @@ struct PairSums {
 };
 struct NoSums {};
 
-template <typename InT, int AT, int NT, int MODE, bool VEC>
+template <typename InT, int AT, int NT, int RS, int MODE, bool VEC>
 struct SweepShared {
   using C = Cfg<InT>;
   static constexpr int L = C::L;
   static constexpr bool REV = MODE == kDv || MODE == kDk;
   using TA = Tile<InT, 32 * AT, REV, VEC>;
-  using TC = Tile<InT, 64 * NT, REV, VEC>;
+  using TC = Tile<InT, 64 * NT / RS, REV, VEC>;
   static constexpr int PSTRIDE = L + 8;
   alignas(16) uint16_t a[C::planes * TA::PLANE];
   alignas(16) uint16_t b[C::planes * TA::PLANE];
@@ -510,24 +519,30 @@ __device__ __forceinline__ f32x4 lds_cols4(const uint16_t* p, int plane) {
   return x;
 }
 
-// Workgroups per CU to allow registers for (LDS holds as many).
-constexpr int sweep_occupancy(int AT, int NT, int bytes) {
-  return bytes == 4 || AT * NT > 4 ? 1 : AT * NT > 2 ? 2 : 3;
+// Workgroups per CU to allow registers for: as many as LDS holds, unless that would spill (a
+// spilled register's reload waits for every load in flight before it).
+constexpr int sweep_occupancy(int AT, int NT, int mode, int bytes) {  // AT * NT <= 8
+  return AT == 8 || (bytes == 4 && mode == kDq && AT * NT >= 4) ? 1
+         : NT == 2 || AT > 2 || bytes == 4 || mode == kDq ? 2 : 3;
 }
 
-template <typename InT, int AT, int NT, int MODE, bool VEC>
-__global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
+// KEEP: the state is kept to 24 bits (it is an output, or goes into the decays' gradient); one that only
+// goes into bf16 outputs takes its inputs in two terms, like its readout.
+template <typename InT, int AT, int NT, int RS, int MODE, bool KEEP, bool VEC>
+__global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, MODE, sizeof(InT)))
     m2rnn_ssm_sweep_kernel(const SsmSweepArgs g) {
   using C = Cfg<InT>;
-  using S = SweepShared<InT, AT, NT, MODE, VEC>;
+  using S = SweepShared<InT, AT, NT, RS, MODE, VEC>;
   using TA = typename S::TA;
   using TC = typename S::TC;
-  constexpr int L = C::L, NI = L / 16, P = C::planes, PS = C::score_terms,
-                PH = MODE == kY || MODE == kDv ? C::state_terms : 3;
+  constexpr int L = C::L, NI = L / 16, NR = NI >= RS ? NI / RS : 1, P = C::planes, PS = C::score_terms,
+                PH = MODE == kY || MODE == kDv ? C::state_terms : 3, CT = KEEP ? 3 : 2;
   __shared__ S sh;
 
   const int lane = threadIdx.x & 63, m = lane & 15, q4 = lane >> 4;
-  const int w = wave_index();
+  // wave: column tiles from 16 NT wc on, and the 16-token rows rg, rg + RS, ... of a chunk's output
+  constexpr int CW = 4 / RS;
+  const int w = wave_index(), wc = w % CW, rg = w / CW;
   // workgroup id -> (b, segment, head, slab), slabs then heads fastest: the heads that
   // share q and k, and the slabs of a head, run on one XCD and share its L2
   int64_t u = xcd_remap((int)blockIdx.x, (int)gridDim.x);
@@ -538,7 +553,7 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
   const int64_t seg = u % g.nseg;
   const int64_t bi = u / g.nseg;
   const int64_t bn = bi * g.N + n;
-  const int c0 = slab * 64 * NT;           // first column of this workgroup
+  const int c0 = slab * (64 * NT / RS);    // first column of this workgroup
   const int dc = g.DC - c0;                // columns left from c0
   constexpr bool REV = S::REV, W_IN = MODE == kY || MODE == kDq, W_OUT = !W_IN;
   constexpr int E = sizeof(InT);
@@ -568,10 +583,13 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
   uint32_t oo[NT], ox[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int col = 16 * (w * NT + nt) + 4 * q4, row = REV ? L - 1 - m : m;
+    const int col = 16 * (wc * NT + nt) + 4 * q4, row = REV ? L - 1 - m : m;
     oo[nt] = col < dc ? (uint32_t)(row * (int)ro.stride) + (uint32_t)(col * oE) : kOut;
     ox[nt] = col < dc ? (uint32_t)(row * (int)re.stride) + (uint32_t)(col * E) : kOut;
   }
+  // the 16-token rows of this wave (fp32's chunks have two: the waves beyond repeat the first ones
+  // and write nothing)
+  auto row_tile = [&](int k) { return NI < RS ? rg % NI : k * RS + rg; };
   const double* cum = g.cum + bn * g.T + t0;
   const float* dts = g.d + bn * g.T + t0;
   const int64_t tok0 = ((int64_t)slab * g.B * g.N + bn) * g.T;  // of the per-token results
@@ -594,12 +612,12 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int ai = 16 * at + 4 * q4 + r, ci = c0 + 16 * (w * NT + nt) + m;
+          const int ai = 16 * at + 4 * q4 + r, ci = c0 + 16 * (wc * NT + nt) + m;
           const bool ok = ai < g.DA && ci < g.DC;
           const int64_t o = (int64_t)ai * g.a_stride + (int64_t)ci * g.c_stride;
           const float x = (s0 && ok) ? s0[o] : 0.0f;
           st[at][nt][r] = x;
-          if (he && ok) dot += (double)x * (double)he[o];
+          if (he && ok && rg == 0) dot += (double)x * (double)he[o];
         }
     if (g.base) {
 #pragma unroll
@@ -619,14 +637,14 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int col = 16 * (w * NT + nt) + 4 * q4 + r;
+      const int col = 16 * (wc * NT + nt) + 4 * q4 + r;
       skip[nt][r] = g.skip && col < dc ? g.skip[(int64_t)n * g.DC + c0 + col] : 0.0f;
     }
 
   TA fa, fb;
   TC fc, fe;
   GateRegs<L, REV> fg;
-  u32x4 ev[MODE == kDk ? NI : 1][NT], ev_next[MODE == kDk ? NI : 1][NT];
+  u32x4 ev[MODE == kDk ? NR : 1][NT];
   float csum[C::epc];
 #pragma unroll
   for (int j = 0; j < C::epc; ++j) csum[j] = 0.0f;
@@ -639,11 +657,11 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
     if constexpr (MODE == kDq) fe.fetch(re, oe, len, dc);
     if constexpr (MODE == kDk) {
 #pragma unroll
-      for (int it = 0; it < NI; ++it)
+      for (int k = 0; k < NR; ++k)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int cc = 16 * (w * NT + nt) + 4 * q4;
-          ev_next[it][nt] = load_cols4<InT>(re, ox[nt], it, 16 * it + m, len, cc, dc - cc);
+          const int cc = 16 * (wc * NT + nt) + 4 * q4, it = row_tile(k);
+          ev[k][nt] = load_cols4<InT>(re, ox[nt], it, 16 * it + m, len, cc, dc - cc);
         }
     }
     fg.fetch(cum, dts, len);
@@ -656,12 +674,6 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
     tf += REV ? -L : L;
   };
   auto put = [&]() {
-    if constexpr (MODE == kDk) {
-#pragma unroll
-      for (int it = 0; it < NI; ++it)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) ev[it][nt] = ev_next[it][nt];
-    }
     fa.put(sh.a);
     fb.put(sh.b);
     fc.put(sh.c);
@@ -678,16 +690,20 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
   for (int ch = 0; ch < nch; ++ch) {
     const int len = chunk_len(t0);
     const Gates<L>& G = sh.g;
-    if (ch + 1 < nch) fetch();
 
-    // scores: tile (it, jt), jt <= it, of a b^T, decayed and split; a wave takes every fourth
-    constexpr int TILES = NI * (NI + 1) / 2;
+    // scores: tile (it, jt), jt <= it, of a b^T, decayed and split.  Wave w takes the diagonal tile
+    // (w, w) and then tiles below the diagonal, so that a tile's kind is known at compile time and
+    // two tiles' products can overlap.
+    {
+    const int ls = fresh(lane), m = ls & 15, q4 = ls >> 4;
+    constexpr int BELOW = NI * (NI - 1) / 2;
 #pragma unroll
-    for (int rd = 0; rd < (TILES + 3) / 4; ++rd) {
-      const int idx = rd * 4 + w;
-      if (idx < TILES) {
-        const int it = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0;
-        const int jt = idx - it * (it + 1) / 2;
+    for (int rd = 0; rd < 1 + (BELOW + 3) / 4; ++rd) {
+      const bool diag = rd == 0;
+      const int idx = diag ? w : NI == 4 ? (rd - 1) * 4 + w : w - 2;
+      if (idx >= 0 && idx < (diag ? NI : BELOW)) {
+        const int it = diag ? idx : idx >= 3 ? 3 : idx >= 1 ? 2 : 1;
+        const int jt = diag ? idx : idx - it * (it - 1) / 2;
         f32x4 s{0, 0, 0, 0};
         const uint16_t* ra = sh.a + (16 * it + m) * TA::STRIDE + 8 * q4;
         const uint16_t* rb = sh.b + (16 * jt + m) * TA::STRIDE + 8 * q4;
@@ -704,7 +720,7 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
         // lane: token i = 16 it + m, inputs j = 16 jt + 4 q4 + r
         const int i = 16 * it + m, j0 = 16 * jt + 4 * q4;
         f32x4 g4{1, 1, 1, 1};  // input weights not yet in s
-        if (it == jt) {
+        if (diag) {
           const f32x4 ch4 = *(const f32x4*)(G.chi + j0), cl4 = *(const f32x4*)(G.clo + j0);
           g4 = *(const f32x4*)(G.g + j0);
           const float hi = G.chi[i], lo = G.clo[i];
@@ -726,7 +742,7 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
           const uint16_t* re = sh.e + (16 * it + m) * TC::STRIDE + 8 * q4;
           const uint16_t* rc = sh.c + (16 * jt + m) * TC::STRIDE + 8 * q4;
 #pragma unroll
-          for (int t = 0; t < 2 * NT; ++t) {
+          for (int t = 0; t < 2 * NT / RS; ++t) {
             bf16x8 xe[P], xc[P];
 #pragma unroll
             for (int p = 0; p < P; ++p) {
@@ -741,7 +757,7 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
           if (m == 0) *(f32x4*)(sh.sums.cs[it] + j0) = col;
           mm *= g4;
           float sum = 0.0f;
-          if (it == jt) {
+          if (diag) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float suf = row_suffix(mm[r]);
@@ -754,7 +770,7 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
             if (q4 == 0) sh.sums.rs[jt][i] = sum;
           }
         }
-        if (MODE == kDq || it == jt) s *= g4;
+        if (MODE == kDq || diag) s *= g4;
         uint32_t x0[PS], x1[PS];
         split2<PS>(s[0], s[1], x0);
         split2<PS>(s[2], s[3], x1);
@@ -763,12 +779,16 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
           *(u32x2*)(sh.p[p] + i * S::PSTRIDE + j0) = u32x2{x0[p], x1[p]};
       }
     }
+    }
+
     // readout of the carried state: lane holds out[i = 16 it + m][c = 4 q4 + r]
-    f32x4 acc[NI][NT];
+    f32x4 acc[NR][NT];
+    {
+    const int ls = fresh(lane), m = ls & 15, q4 = ls >> 4;
 #pragma unroll
-    for (int it = 0; it < NI; ++it)
+    for (int k = 0; k < NR; ++k)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) acc[it][nt] = f32x4{0, 0, 0, 0};
+      for (int nt = 0; nt < NT; ++nt) acc[k][nt] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int t = 0; t < AT; ++t) {
       bf16x8 hs[NT][PH];
@@ -779,46 +799,54 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
         split8<PH>(x, hs[nt]);
       }
 #pragma unroll
-      for (int it = 0; it < NI; ++it) {
+      for (int k = 0; k < NR; ++k) {
+        const int row = 16 * row_tile(k) + m;
         bf16x8 xa[P];
 #pragma unroll
         for (int p = 0; p < P; ++p)
-          xa[p] = row4x2(sh.a + p * TA::PLANE + (16 * it + m) * TA::STRIDE + 32 * t + 4 * q4);
+          xa[p] = row4x2(sh.a + p * TA::PLANE + row * TA::STRIDE + 32 * t + 4 * q4);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[it][nt] = mfma_terms(hs[nt], xa, acc[it][nt]);
+        for (int nt = 0; nt < NT; ++nt) acc[k][nt] = mfma_terms(hs[nt], xa, acc[k][nt]);
       }
     }
 #pragma unroll
-    for (int it = 0; it < NI; ++it) {
-      const float R = G.R[16 * it + m];
+    for (int k = 0; k < NR; ++k) {
+      const float R = G.R[16 * row_tile(k) + m];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) acc[it][nt] *= R;
+      for (int nt = 0; nt < NT; ++nt) acc[k][nt] *= R;
     }
     if constexpr ((MODE == kDk || MODE == kDq)) {
       // e . (the state's part of the output), this wave's columns
 #pragma unroll
-      for (int it = 0; it < NI; ++it) {
-        const int i = 16 * it + m;
+      for (int k = 0; k < NR; ++k) {
+        const int i = 16 * row_tile(k) + m;
         float dot = 0.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int cc = 16 * (w * NT + nt) + 4 * q4;
+          const int cc = 16 * (wc * NT + nt) + 4 * q4;
           f32x4 y;
           if constexpr (MODE == kDq) y = lds_cols4<P>(sh.e + i * TC::STRIDE + cc, TC::PLANE);
-          else y = widen4<InT>(ev[it][nt]);
-          const f32x4 x = acc[it][nt];
+          else y = widen4<InT>(ev[k][nt]);
+          const f32x4 x = acc[k][nt];
           dot += (y[0] * x[0] + y[1] * x[1]) + (y[2] * x[2] + y[3] * x[3]);
         }
         dot = rows_sum(dot);
-        if (q4 == 0) sh.red[w][i] = dot;
+        if (q4 == 0) sh.red[wc][i] = dot;
       }
     }
+    }
     lds_barrier();  // the scores are in LDS
+    // the next chunk's tiles, here rather than before the scores: their registers are free in the
+    // first half, and the second is longer than the loads take
+    if (ch + 1 < nch) fetch();
 
     if constexpr ((MODE == kDk || MODE == kDq)) {
       if (w == 2 && lane < len) {
         const int64_t o = tok0 + t0 + (REV ? len - 1 - lane : lane);
-        g.rowdot[o] = (sh.red[0][lane] + sh.red[1][lane]) + (sh.red[2][lane] + sh.red[3][lane]);
+        float sum = sh.red[0][lane];
+#pragma unroll
+        for (int i = 1; i < CW; ++i) sum += sh.red[i][lane];
+        g.rowdot[o] = sum;
       }
     }
     if constexpr (MODE == kDq) {
@@ -849,6 +877,8 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
     }
 
     // the chunk's own inputs, and what they leave in the state
+    {
+    const int ls = fresh(lane), m = ls & 15, q4 = ls >> 4;
     const float ftot = G.total;
 #pragma unroll
     for (int at = 0; at < 2 * AT; ++at)
@@ -856,7 +886,7 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
       for (int nt = 0; nt < NT; ++nt) st[at][nt] *= ftot;
 #pragma unroll
     for (int jb = 0; jb < L / 32; ++jb) {
-      bf16x8 cw[NT][3];
+      bf16x8 cw[NT][CT];
       const f32x4 w0 = *(const f32x4*)(G.W + 32 * jb + 8 * q4),
                   w1 = *(const f32x4*)(G.W + 32 * jb + 8 * q4 + 4);
 #pragma unroll
@@ -864,46 +894,55 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
         bf16x8 xc[P];
 #pragma unroll
         for (int p = 0; p < P; ++p)
-          xc[p] = col8(sh.c + p * TC::PLANE + (32 * jb + 8 * q4) * TC::STRIDE + 16 * (w * NT + nt),
+          xc[p] = col8(sh.c + p * TC::PLANE + (32 * jb + 8 * q4) * TC::STRIDE + 16 * (wc * NT + nt),
                        TC::STRIDE, m);
 #pragma unroll
-        for (int it = 2 * jb; it < NI; ++it) {
-          bf16x8 xp[PS];
+        for (int k = 0; k < NR; ++k) {
+          const int it = row_tile(k);
+          if (it >= 2 * jb) {
+            bf16x8 xp[PS];
 #pragma unroll
-          for (int p = 0; p < PS; ++p)
-            xp[p] = row8(sh.p[p] + (16 * it + m) * S::PSTRIDE + 32 * jb + 8 * q4);
-          acc[it][nt] = mfma_terms(xc, xp, acc[it][nt]);
+            for (int p = 0; p < PS; ++p)
+              xp[p] = row8(sh.p[p] + (16 * it + m) * S::PSTRIDE + 32 * jb + 8 * q4);
+            acc[k][nt] = mfma_terms(xc, xp, acc[k][nt]);
+          }
         }
         float x[8];
         widen8<P>(xc, x);
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] *= j < 4 ? w0[j & 3] : w1[j & 3];
-        split8<3>(x, cw[nt]);
+        split8<CT>(x, cw[nt]);
       }
 #pragma unroll
       for (int at = 0; at < 2 * AT; ++at) {
         bf16x8 xb[P];
 #pragma unroll
         for (int p = 0; p < P; ++p)
-          xb[p] = col8(sh.b + p * TA::PLANE + (32 * jb + 8 * q4) * TA::STRIDE + 16 * at, TA::STRIDE, m);
+          xb[p] = col8(sh.b + p * TA::PLANE + (32 * jb + 8 * q4) * TA::STRIDE + 16 * at,
+                       TA::STRIDE, m);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) st[at][nt] = mfma_terms(xb, cw[nt], st[at][nt]);
       }
     }
+    }
 
     // output
+    {
+    const int ls = fresh(lane), m = ls & 15, q4 = ls >> 4;
 #pragma unroll
-    for (int it = 0; it < NI; ++it) {
-      const int i = 16 * it + m;
+    for (int k = 0; k < NR; ++k) {
+      const int it = row_tile(k), i = 16 * it + m;
+      if (NI < RS && rg >= NI) break;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int cc = 16 * (w * NT + nt) + 4 * q4;
-        f32x4 x = acc[it][nt];
+        const int cc = 16 * (wc * NT + nt) + 4 * q4;
+        f32x4 x = acc[k][nt];
         if constexpr (W_OUT) x *= G.rho[i];
         if constexpr (MODE == kY || MODE == kDv)
           x += skip[nt] * lds_cols4<P>(sh.c + i * TC::STRIDE + cc, TC::PLANE);
         store_cols4<InT>(ro, oo[nt], it, i, len, x, cc, dc - cc, oE > E);
       }
+    }
     }
     ro.next();
     t0 += REV ? -L : L;
@@ -914,7 +953,7 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
     }
   }
 
-  if (g.stateT) {
+  if (g.stateT && rg == 0) {
     float* sT = g.stateT + bn * (int64_t)g.DA * g.DC;
 #pragma unroll
     for (int at = 0; at < 2 * AT; ++at)
@@ -922,7 +961,7 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int ai = 16 * at + 4 * q4 + r, ci = c0 + 16 * (w * NT + nt) + m;
+          const int ai = 16 * at + 4 * q4 + r, ci = c0 + 16 * (wc * NT + nt) + m;
           if (ai < g.DA && ci < g.DC)
             sT[(int64_t)ai * g.a_stride + (int64_t)ci * g.c_stride] = st[at][nt][r];
         }
@@ -942,12 +981,12 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, sizeof(InT)))
 }
 
 // The state a segment adds to a zero start: the sweep's state update alone.
-template <typename InT, int AT, int NT, bool REV, bool VEC>
+template <typename InT, int AT, int NT, int RS, bool REV, bool VEC>
 __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 1)
     m2rnn_ssm_contrib_kernel(const SsmContribArgs g) {
   using C = Cfg<InT>;
   using TB = Tile<InT, 32 * AT, REV, VEC>;
-  using TC = Tile<InT, 64 * NT, REV, VEC>;
+  using TC = Tile<InT, 64 * NT / RS, REV, VEC>;
   constexpr int L = C::L, P = C::planes, E = sizeof(InT);
   struct Sh {
     alignas(16) uint16_t b[P * TB::PLANE];
@@ -956,7 +995,9 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
   };
   __shared__ Sh sh;
   const int lane = threadIdx.x & 63, m = lane & 15, q4 = lane >> 4;
-  const int w = wave_index();
+  // wave: column tiles from 16 NT wc on, state rows from 16 HA rg on
+  constexpr int CW = 4 / RS, HA = 2 * AT / RS;
+  const int w = wave_index(), wc = w % CW, rg = w / CW;
   int64_t u = xcd_remap((int)blockIdx.x, (int)gridDim.x);
   const int slab = (int)(u % g.slabs);
   u /= g.slabs;
@@ -965,7 +1006,7 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
   const int64_t seg = u % g.nseg;
   const int64_t bi = u / g.nseg;
   const int64_t bn = bi * g.N + n;
-  const int c0 = slab * 64 * NT;
+  const int c0 = slab * (64 * NT / RS);
   const int64_t seg0 = seg * g.seglen;
   const int64_t seg1 = seg0 + g.seglen < g.T ? seg0 + g.seglen : g.T;
   const int nch = (int)((seg1 - seg0 + L - 1) / L);
@@ -981,9 +1022,9 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
   const double* cum = g.cum + bn * g.T + tf;
   const float* dts = g.d + bn * g.T + tf;
 
-  f32x4 st[2 * AT][NT];
+  f32x4 st[HA][NT];
 #pragma unroll
-  for (int at = 0; at < 2 * AT; ++at)
+  for (int at = 0; at < HA; ++at)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) st[at][nt] = f32x4{0, 0, 0, 0};
   float ftot = 1.0f;
@@ -1015,7 +1056,7 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
     const float f = G.total;
     ftot *= f;
 #pragma unroll
-    for (int at = 0; at < 2 * AT; ++at)
+    for (int at = 0; at < HA; ++at)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) st[at][nt] *= f;
 #pragma unroll
@@ -1028,7 +1069,7 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
         bf16x8 xc[P];
 #pragma unroll
         for (int p = 0; p < P; ++p)
-          xc[p] = col8(sh.c + p * TC::PLANE + (32 * jb + 8 * q4) * TC::STRIDE + 16 * (w * NT + nt),
+          xc[p] = col8(sh.c + p * TC::PLANE + (32 * jb + 8 * q4) * TC::STRIDE + 16 * (wc * NT + nt),
                        TC::STRIDE, m);
         float x[8];
         widen8<P>(xc, x);
@@ -1037,11 +1078,11 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
         split8<3>(x, cw[nt]);
       }
 #pragma unroll
-      for (int at = 0; at < 2 * AT; ++at) {
+      for (int at = 0; at < HA; ++at) {
         bf16x8 xb[P];
 #pragma unroll
         for (int p = 0; p < P; ++p)
-          xb[p] = col8(sh.b + p * TB::PLANE + (32 * jb + 8 * q4) * TB::STRIDE + 16 * at, TB::STRIDE, m);
+          xb[p] = col8(sh.b + p * TB::PLANE + (32 * jb + 8 * q4) * TB::STRIDE + 16 * (HA * rg + at), TB::STRIDE, m);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) st[at][nt] = mfma_terms(xb, cw[nt], st[at][nt]);
       }
@@ -1054,12 +1095,12 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
   }
   float* o = g.contrib + (bn * g.nseg + seg) * (int64_t)g.DA * g.DC;
 #pragma unroll
-  for (int at = 0; at < 2 * AT; ++at)
+  for (int at = 0; at < HA; ++at)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int ai = 16 * at + 4 * q4 + r, ci = c0 + 16 * (w * NT + nt) + m;
+        const int ai = 16 * (HA * rg + at) + 4 * q4 + r, ci = c0 + 16 * (wc * NT + nt) + m;
         if (ai < g.DA && ci < g.DC) o[(int64_t)ai * g.DC + ci] = st[at][nt][r];
       }
   if (g.fseg && slab == 0 && threadIdx.x == 0) g.fseg[bn * g.nseg + seg] = ftot;

@@ -10,17 +10,30 @@ namespace {
 #define M2RNN_SSM_NAME launch_ssm_sweep_bf16
 #endif
 
-template <typename InT, int AT, int NT, int MODE>
+template <typename InT, int AT, int NT, int RS, int MODE>
 hipError_t run(const SsmSweepArgs& a, hipStream_t stream) {
-  const int64_t grid = a.B * a.N * a.nseg * a.slabs;
-  hipLaunchKernelGGL((ssm::m2rnn_ssm_sweep_kernel<InT, AT, NT, MODE, M2RNN_SSM_VEC>), dim3((unsigned)grid),
+  const dim3 grid((unsigned)(a.B * a.N * a.nseg * a.slabs));
+  if constexpr (sizeof(InT) == 2 && (MODE == ssm::kY || MODE == ssm::kDv))
+    if (!a.stateT) {
+      hipLaunchKernelGGL((ssm::m2rnn_ssm_sweep_kernel<InT, AT, NT, RS, MODE, false, M2RNN_SSM_VEC>),
+                         grid, dim3(256), 0, stream, a);
+      return hipGetLastError();
+    }
+  hipLaunchKernelGGL((ssm::m2rnn_ssm_sweep_kernel<InT, AT, NT, RS, MODE, true, M2RNN_SSM_VEC>), grid,
                      dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
+// Columns per workgroup (ssm_columns), and how many waves share them when there are few; dq
+// contracts over them in blocks of 32.
 template <typename InT, int AT, int MODE>
 hipError_t pick_nt(const SsmSweepArgs& a, hipStream_t stream) {
-  return a.DC <= 64 ? run<InT, AT, 1, MODE>(a, stream) : run<InT, AT, 2, MODE>(a, stream);
+  if constexpr (AT <= 2)
+    if (ssm_columns(a.DA, a.DC) == 128) return run<InT, AT, 2, 1, MODE>(a, stream);
+  if constexpr (MODE != ssm::kDq)
+    if (a.DC <= 16) return run<InT, AT, 1, 4, MODE>(a, stream);
+  if (a.DC <= 32) return run<InT, AT, 1, 2, MODE>(a, stream);
+  return run<InT, AT, 1, 1, MODE>(a, stream);
 }
 
 template <typename InT, int MODE>
