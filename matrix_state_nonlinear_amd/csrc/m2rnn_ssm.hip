@@ -59,45 +59,59 @@ __global__ void __launch_bounds__(256)
   }
   __syncthreads();
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  float dt[4];
+  double sum[4];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const int64_t n = n0 + 4 * w + h < N ? n0 + 4 * w + h : N - 1;
+    dt[h] = ssm::softplus(x[lane][4 * w + h] + beta[n]);
+    sum[h] = t0 + lane < T ? ssm::log2_decay(alpha[n], dt[h]) : 0.0;
+  }
+#pragma unroll
+  for (int s = 1; s < L; s *= 2)
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const double o = __shfl_up(sum[h], s);
+      if ((lane & (L - 1)) >= s) sum[h] += o;
+    }
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     const int64_t n = n0 + 4 * w + h;
-    if (n >= N) return;
-    const float dt = ssm::softplus(x[lane][4 * w + h] + beta[n]);
-    double sum = t0 + lane < T ? ssm::log2_decay(alpha[n], dt) : 0.0;
-#pragma unroll
-    for (int s = 1; s < L; s *= 2) {
-      const double o = __shfl_up(sum, s);
-      if ((lane & (L - 1)) >= s) sum += o;
-    }
-    if (t0 + lane < T) {
+    if (n < N && t0 + lane < T) {
       const int64_t at = (b * N + n) * T + t0 + lane;
-      cum[at] = sum;
-      d[at] = dt;
+      cum[at] = sum[h];
+      d[at] = dt[h];
     }
   }
 }
 
-// seg[u][s] (what segment s adds) -> the state at its start (rev: at its end, from later
-// segments); last[u] the state after all of them.  One thread per state element.
+// One thread per state element; blockIdx.y the scan.  Loads run four segments ahead of the sums.
 __global__ void __launch_bounds__(256)
-    m2rnn_ssm_segscan_kernel(float* __restrict__ seg, const float* __restrict__ fseg,
-                             const float* __restrict__ first, float* __restrict__ last,
-                             int64_t total, int64_t nseg, int64_t KV, int rev) {
+    m2rnn_ssm_segscan_kernel(const SsmSegScans scans, const float* __restrict__ fseg, int64_t total,
+                             int64_t nseg, int64_t KV) {
+  const SsmSegScan sc = scans.s[blockIdx.y];
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= total) return;
   const int64_t u = i / KV, x = i % KV;
-  float cur = first ? first[i] : 0.0f;
-  float* p = seg + u * nseg * KV + x;
+  float cur = sc.first ? sc.first[i] : 0.0f;
+  float* p = sc.seg + u * nseg * KV + x;
   const float* f = fseg + u * nseg;
-#pragma unroll 4
-  for (int64_t s = 0; s < nseg; ++s) {
-    const int64_t j = rev ? nseg - 1 - s : s;
-    const float add = p[j * KV];
-    p[j * KV] = cur;
-    cur = __builtin_fmaf(f[j], cur, add);
+  for (int64_t s = 0; s < nseg; s += 4) {
+    float add[4], fs[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t q = s + k < nseg ? s + k : nseg - 1, j = sc.rev ? nseg - 1 - q : q;
+      add[k] = p[j * KV];
+      fs[k] = f[j];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (s + k < nseg) {
+        p[(sc.rev ? nseg - 1 - (s + k) : s + k) * KV] = cur;
+        cur = __builtin_fmaf(fs[k], cur, add[k]);
+      }
   }
-  if (last) last[i] = cur;
+  if (sc.last) sc.last[i] = cur;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -109,12 +123,12 @@ hipError_t launch_ssm_contrib(const SsmContribArgs& a, int in_dtype, hipStream_t
   return in_dtype == kBF16 ? pick_at<uint16_t>(a, stream) : pick_at<float>(a, stream);
 }
 
-hipError_t launch_ssm_segscan(float* seg, const float* fseg, const float* first, float* last,
-                              int64_t units, int64_t nseg, int64_t KV, bool rev,
-                              hipStream_t stream) {
+hipError_t launch_ssm_segscan(const SsmSegScans& scans, const float* fseg, int64_t units,
+                              int64_t nseg, int64_t KV, hipStream_t stream) {
   const int64_t total = units * KV;
-  hipLaunchKernelGGL(m2rnn_ssm_segscan_kernel, dim3((unsigned)ceil_div(total, 256)), dim3(256), 0,
-                     stream, seg, fseg, first, last, total, nseg, KV, rev ? 1 : 0);
+  hipLaunchKernelGGL(m2rnn_ssm_segscan_kernel,
+                     dim3((unsigned)ceil_div(total, 256), scans.s[1].seg ? 2 : 1), dim3(256), 0,
+                     stream, scans, fseg, total, nseg, KV);
   return hipGetLastError();
 }
 
@@ -189,7 +203,8 @@ hipError_t launch_ssm_fwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
     c.DA = (int)a.K; c.DC = (int)a.V; c.w_in = 1;
     c.vec = vk && vv;
     if ((err = launch_ssm_contrib(c, in_dtype, stream)) != hipSuccess) return err;
-    err = launch_ssm_segscan(hseg, fseg, a.H0, a.HT, a.B * a.N, L.nseg, a.K * a.V, false, stream);
+    err = launch_ssm_segscan({{{hseg, a.H0, a.HT, false}, {}}}, fseg, a.B * a.N, L.nseg, a.K * a.V,
+                             stream);
     if (err != hipSuccess) return err;
     start = hseg;
   }

@@ -18,15 +18,15 @@ namespace m2rnn {
 
 namespace {
 
-constexpr int64_t kMaxSeg = 512;  // tokens per segment at most
+constexpr int64_t kMaxSeg = 512;  // tokens per segment at most (16 chunks of 32 in the kernel below)
 constexpr double kNoPass = 15.0;  // -log of 3e-7
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t pad64(size_t x) { return align_up(x, 64); }
 
-// One wave per (b, n, segment), from its last chunk to its first (chunks of `L` tokens, as
-// in the sweeps).
-__global__ void __launch_bounds__(256)
+// One workgroup per (b, n, segment), a wave per chunk of `L` tokens (as in the sweeps): the sums
+// inside the chunks all at once, then every wave follows w from the segment's end to its chunk.
+__global__ void __launch_bounds__(1024)
     m2rnn_ssm_dgate_kernel(int64_t B, int64_t T, int64_t N, int64_t nseg, int64_t seglen, int L,
                            int slabs, int vslabs, const float* __restrict__ adot,
                            const float* __restrict__ bdot, const float* __restrict__ pairs,
@@ -34,59 +34,67 @@ __global__ void __launch_bounds__(256)
                            const float* __restrict__ logit, const float* __restrict__ alpha,
                            const float* __restrict__ beta, float* __restrict__ dlogit,
                            float* __restrict__ part) {
-  // heads fastest: the waves of a workgroup share lines of logit and dlogit
-  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (unit >= B * N * nseg) return;
-  const int lane = threadIdx.x & 63;
+  __shared__ double tot[3][16];  // per chunk: sums of a and b, and its -log f in all
+  __shared__ double red[2][16];
+  // heads fastest: neighbouring workgroups share lines of logit and dlogit
+  const int64_t unit = blockIdx.x;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t n = unit % N, seg = unit / N % nseg, b = unit / N / nseg;
   const int64_t bn = b * N + n;
   const int64_t t0 = seg * seglen, t1 = t0 + seglen < T ? t0 + seglen : T;
-  const float al = alpha[n], be = beta[n];
-  double w_end = 0.0;
+  const int nch = (int)((t1 - t0 + L - 1) / L);
+  const int64_t c = t0 + (int64_t)w * L;
+  // lane 0 has the chunk's last token
+  const int len = c < t1 ? (int)(t1 - c < L ? t1 - c : L) : 0;
+  const int64_t t = c + len - 1 - lane;
+  const bool ok = lane < len;
+  const double al = (double)alpha[n];
+  double a = 0.0, dd = 0.0, bs = 0.0, X = 0.0;
+  float x = 0.0f;
+  if (ok) {
+    for (int s = 0; s < slabs; ++s) {
+      const int64_t o = ((int64_t)s * B * N + bn) * T + t;
+      a += (double)adot[o];
+      bs += (double)bdot[o];
+      dd += (double)colpairs[o];
+      X += (double)pairs[o];
+    }
+    x = logit[(b * T + t) * N + n] + beta[n];
+  }
+  const float d = ok ? ssm::softplus(x) : 0.0f;
+  dd += bs;
+  // asum: a from this token on; bsum: b before this token; decay: the chunk's -log f in all
+  double asum = a, bsum = bs * (double)d, decay = al * (double)d;
+  const double b_own = bsum;
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) {
+    const double oa = __shfl_up(asum, s), ob = __shfl_down(bsum, s);
+    if (lane >= s) asum += oa;
+    if (lane + s < 64) bsum += ob;
+    decay += __shfl_xor(decay, s);
+  }
+  if (lane == 0) {
+    tot[1][w] = bsum;
+    tot[2][w] = decay;
+  }
+  if (lane == 63) tot[0][w] = asum;
+  bsum -= b_own;
+  __syncthreads();
+  double w_end = 0.0, g = 0.0;
   if (base)
     for (int s = 0; s < vslabs; ++s) w_end += (double)base[((int64_t)s * B * N + bn) * nseg + seg];
+  for (int k = nch - 1; k >= w; --k) {
+    g = tot[2][k] > kNoPass ? 0.0 : w_end - tot[1][k];
+    w_end = tot[0][k] + g;
+  }
   double sa = 0.0, sb = 0.0;
-  for (int64_t c = t0 + (t1 - t0 - 1) / L * L; c >= t0; c -= L) {
-    // lane 0 has the chunk's last token
-    const int len = (int)(t1 - c < L ? t1 - c : L);
-    const int64_t t = c + len - 1 - lane;
-    const bool ok = lane < len;
-    double a = 0.0, dd = 0.0, bs = 0.0, X = 0.0;
-    float x = 0.0f;
-    if (ok) {
-      for (int s = 0; s < slabs; ++s) {
-        const int64_t o = ((int64_t)s * B * N + bn) * T + t;
-        a += (double)adot[o];
-        bs += (double)bdot[o];
-        dd += (double)colpairs[o];
-        X += (double)pairs[o];
-      }
-      x = logit[(b * T + t) * N + n] + be;
-    }
-    const float d = ssm::softplus(x);
-    dd += bs;
-    // asum: a from this token on; bsum: b before this token; decay: the chunk's -log f in all
-    double asum = a, bsum = bs * (double)d, decay = ok ? (double)al * (double)d : 0.0;
-    const double b_own = bsum;
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) {
-      const double oa = __shfl_up(asum, s), ob = __shfl_down(bsum, s);
-      if (lane >= s) asum += oa;
-      if (lane + s < 64) bsum += ob;
-      decay += __shfl_xor(decay, s);
-    }
-    const double g = decay > kNoPass ? 0.0 : w_end - __shfl(bsum, 0);
-    bsum -= b_own;
-    if (ok) {
-      const double dl = X + asum + (bsum + g);
-      const float ex = expf(-fabsf(x));
-      const float sig = x >= 0.0f ? 1.0f / (1.0f + ex) : ex / (1.0f + ex);
-      const double dx = (double)sig * (dd - (double)al * dl);
-      dlogit[(b * T + t) * N + n] = (float)dx;
-      sa -= (double)d * dl;
-      sb += dx;
-    }
-    w_end = __shfl(asum, 63) + g;
+  if (ok) {
+    const double dl = X + asum + (bsum + g);
+    const float ex = expf(-fabsf(x));
+    const float sig = x >= 0.0f ? 1.0f / (1.0f + ex) : ex / (1.0f + ex);
+    sb = (double)sig * (dd - al * dl);
+    sa = -(double)d * dl;
+    dlogit[(b * T + t) * N + n] = (float)sb;
   }
 #pragma unroll
   for (int s = 1; s < 64; s *= 2) {
@@ -94,8 +102,14 @@ __global__ void __launch_bounds__(256)
     sb += __shfl_xor(sb, s);
   }
   if (lane == 0) {
-    part[(bn * nseg + seg) * 2] = (float)sa;
-    part[(bn * nseg + seg) * 2 + 1] = (float)sb;
+    red[0][w] = sa;
+    red[1][w] = sb;
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    double sum = 0.0;
+    for (int k = 0; k < nch; ++k) sum += red[threadIdx.x][k];
+    part[(bn * nseg + seg) * 2 + threadIdx.x] = (float)sum;
   }
 }
 
@@ -226,9 +240,8 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
     c.b = a.q; c.c = a.dy;
     c.contrib = gseg; c.fseg = nullptr; c.w_in = 0; c.rev = 1;
     if ((err = launch_ssm_contrib(c, in_dtype, stream)) != hipSuccess) return err;
-    err = launch_ssm_segscan(hseg, fseg, a.H0, hT, units, L.nseg, KV, false, stream);
-    if (err != hipSuccess) return err;
-    err = launch_ssm_segscan(gseg, fseg, a.dHT, a.dH0, units, L.nseg, KV, true, stream);
+    err = launch_ssm_segscan({{{hseg, a.H0, hT, false}, {gseg, a.dHT, a.dH0, true}}}, fseg, units,
+                             L.nseg, KV, stream);
     if (err != hipSuccess) return err;
   }
 
@@ -286,12 +299,13 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
   dk.vec = vec && vdk;
   if ((err = launch_ssm_sweep(dk, in_dtype, stream)) != hipSuccess) return err;
 
-  hipLaunchKernelGGL(m2rnn_ssm_dgate_kernel, dim3((unsigned)ceil_div(units * L.nseg, 4)),
-                     dim3(256), 0, stream, a.B, a.T, a.N, L.nseg, L.seglen,
-                     in_dtype == kBF16 ? ssm::Cfg<uint16_t>::L : ssm::Cfg<float>::L,
-                     (int)ssm_slabs(a.V, a.K), (int)ssm_slabs(a.K, a.V), a.ws + L.adot, a.ws + L.bdot,
-                     a.ws + L.pairs, a.ws + L.colpairs, passes ? a.ws + L.base : nullptr, a.logit,
-                     a.alpha, a.beta, a.dlogit, a.ws + L.gatepart);
+  const int chunk = in_dtype == kBF16 ? ssm::Cfg<uint16_t>::L : ssm::Cfg<float>::L;
+  hipLaunchKernelGGL(m2rnn_ssm_dgate_kernel, dim3((unsigned)(units * L.nseg)),
+                     dim3((unsigned)(64 * ceil_div(L.seglen, chunk))), 0, stream, a.B, a.T, a.N,
+                     L.nseg, L.seglen, chunk, (int)ssm_slabs(a.V, a.K), (int)ssm_slabs(a.K, a.V),
+                     a.ws + L.adot, a.ws + L.bdot, a.ws + L.pairs, a.ws + L.colpairs,
+                     passes ? a.ws + L.base : nullptr, a.logit, a.alpha, a.beta, a.dlogit,
+                     a.ws + L.gatepart);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   hipLaunchKernelGGL(m2rnn_ssm_params_kernel, dim3((unsigned)(a.N * ceil_div(a.V + 2, 64))),
                      dim3(256), 0, stream, a.B, a.N, L.nseg, a.V, a.ws + L.colsum,

@@ -136,8 +136,19 @@ hipError_t launch_ssm_decays(const SsmArgs& a, int in_dtype, double* cum, float*
 // Whether rows of `heads` x `D` elements at p can be accessed in 16-byte pieces with 32-bit offsets
 // within a chunk.
 bool ssm_vec_rows(const void* p, int64_t heads, int64_t D, int elem_bytes);
-hipError_t launch_ssm_segscan(float* seg, const float* fseg, const float* first, float* last,
-                              int64_t units, int64_t nseg, int64_t KV, bool rev,
-                              hipStream_t stream);
+// Scans over the segments, one or two in a launch: seg [units, nseg, KV] (what a segment adds)
+// becomes the state each starts from (rev: ends at), `first` [units, KV] or null = 0 the first
+// one's, and `last` [units, KV] or null gets the state behind the last.
+struct SsmSegScan {
+  float* seg;
+  const float* first;
+  float* last;
+  bool rev;
+};
+struct SsmSegScans {
+  SsmSegScan s[2];
+};
+hipError_t launch_ssm_segscan(const SsmSegScans& scans, const float* fseg, int64_t units,
+                              int64_t nseg, int64_t KV, hipStream_t stream);
 
 }  // namespace m2rnn

@@ -968,7 +968,8 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, MODE, sizeof(InT)
   }
   if (do_col) {  // threads with the same columns: 256 / CPR of them, summed in order
     lds_barrier();
-    float* red = (float*)sh.a;
+    static_assert(sizeof(sh.a) + sizeof(sh.b) >= 256 * C::epc * sizeof(float), "");
+    float* red = (float*)&sh;  // over a and b, which nobody reads any more
 #pragma unroll
     for (int j = 0; j < C::epc; ++j) red[threadIdx.x * C::epc + j] = csum[j];
     lds_barrier();
@@ -980,7 +981,10 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, MODE, sizeof(InT)
   }
 }
 
-// The state a segment adds to a zero start: the sweep's state update alone.
+// The state a segment adds to a zero start: the sweep's state update alone.  Both directions
+// walk from the segment's last chunk to its first: with forward decays a chunk's inputs are
+// weighted by all that follows (`run`), and the sweep that comes next, walking forward, finds
+// the tokens read last in the memory-side cache.
 template <typename InT, int AT, int NT, int RS, bool REV, bool VEC>
 __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 1)
     m2rnn_ssm_contrib_kernel(const SsmContribArgs g) {
@@ -1011,7 +1015,7 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
   const int64_t seg1 = seg0 + g.seglen < g.T ? seg0 + g.seglen : g.T;
   const int nch = (int)((seg1 - seg0 + L - 1) / L);
   const int dc = g.DC - c0;
-  int64_t tf = seg0 + (REV ? (int64_t)(nch - 1) * L : 0);
+  int64_t tf = seg0 + (int64_t)(nch - 1) * L;
   auto walk = [&](const void* p, int grp, int D, int col) {
     const int64_t heads = g.N / grp;
     return Walk<L, REV, VEC>{(const char*)p + (((bi * g.T + tf) * heads + n / grp) * D + col) * E,
@@ -1036,11 +1040,11 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
     fb.fetch(rb, ob, len, g.DA);
     fc.fetch(rc, oc, len, dc);
     fg.fetch(cum, dts, len);
-    rb.next();
-    rc.next();
-    cum += REV ? -L : L;
-    dts += REV ? -L : L;
-    tf += REV ? -L : L;
+    rb.base -= L * (int64_t)rb.stride;
+    rc.base -= L * (int64_t)rc.stride;
+    cum -= L;
+    dts -= L;
+    tf -= L;
   };
   auto put = [&]() {
     fb.put(sh.b);
@@ -1053,17 +1057,22 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
   for (int ch = 0; ch < nch; ++ch) {
     const Gates<L>& G = sh.g;
     if (ch + 1 < nch) fetch();
-    const float f = G.total;
+    const float f = G.total, run = REV ? 1.0f : ftot;
     ftot *= f;
+    if constexpr (REV)
 #pragma unroll
-    for (int at = 0; at < HA; ++at)
+      for (int at = 0; at < HA; ++at)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) st[at][nt] *= f;
+        for (int nt = 0; nt < NT; ++nt) st[at][nt] *= f;
 #pragma unroll
     for (int jb = 0; jb < L / 32; ++jb) {
       bf16x8 cw[NT][3];
-      const f32x4 w0 = *(const f32x4*)(G.W + 32 * jb + 8 * q4),
-                  w1 = *(const f32x4*)(G.W + 32 * jb + 8 * q4 + 4);
+      f32x4 w0 = *(const f32x4*)(G.W + 32 * jb + 8 * q4),
+            w1 = *(const f32x4*)(G.W + 32 * jb + 8 * q4 + 4);
+      if constexpr (!REV) {
+        w0 *= run;
+        w1 *= run;
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         bf16x8 xc[P];
