@@ -143,7 +143,7 @@ bool newton_supported(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
 bool ssm_supported(int64_t B, int64_t T, int64_t N, int64_t NQ, int64_t K, int64_t V) {
   if (!sizes_supported(B, T, N, K, V)) return false;
   if (B * T * N == 0) return true;
-  const SsmLayout L = ssm_bwd_layout(B, T, N, NQ, K, V, M2RNN_F32);
+  const SsmLayout L = ssm_bwd_layout(B, T, N, NQ, K, V);
   return 4.0 * (double)B * (double)N * (double)L.nseg < (double)(1 << 24) &&
          (double)B * (double)T * (double)NQ * (double)K < 4294967296.0 &&
          (double)B * (double)N * (double)K * (double)V < 4294967296.0;
@@ -512,7 +512,7 @@ size_t m2rnn_ssm_workspace_bytes(int is_bwd, int64_t B, int64_t T, int64_t n_hea
       !dtypes_ok(in_dtype, M2RNN_F32) || !ssm_supported(B, T, n_heads, qk_heads, K, V) ||
       B * T * n_heads == 0)
     return 0;
-  const SsmLayout L = is_bwd ? ssm_bwd_layout(B, T, n_heads, qk_heads, K, V, in_dtype)
+  const SsmLayout L = is_bwd ? ssm_bwd_layout(B, T, n_heads, qk_heads, K, V)
                              : ssm_fwd_layout(B, T, n_heads, K, V, in_dtype);
   return align_up(L.total_floats * 4, 256);
 }
@@ -568,7 +568,7 @@ int m2rnn_ssm_bwd(int64_t B, int64_t T, int64_t n_heads, int64_t qk_heads, int64
     if (e == hipSuccess) e = fill(dbeta, nullptr, n_heads, M2RNN_F32, st);
     return status_of(e);
   }
-  const SsmLayout L = ssm_bwd_layout(B, T, n_heads, qk_heads, K, V, in_dtype);
+  const SsmLayout L = ssm_bwd_layout(B, T, n_heads, qk_heads, K, V);
   const size_t need = align_up(L.total_floats * 4, 256);
   if (!workspace || workspace_bytes < need) return M2RNN_ERR_WORKSPACE;
   if (!aligned16(workspace)) return M2RNN_ERR_INVALID_ARG;

@@ -68,12 +68,7 @@ __global__ void __launch_bounds__(256)
     sum[h] = t0 + lane < T ? ssm::log2_decay(alpha[n], dt[h]) : 0.0;
   }
 #pragma unroll
-  for (int s = 1; s < L; s *= 2)
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const double o = __shfl_up(sum[h], s);
-      if ((lane & (L - 1)) >= s) sum[h] += o;
-    }
+  for (int h = 0; h < 4; ++h) sum[h] = ssm::lane_sums<L>(sum[h]);
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     const int64_t n = n0 + 4 * w + h;

@@ -321,6 +321,27 @@ __device__ __forceinline__ double log2_decay(float alpha, float d) {
   return fmax(-(double)alpha * (double)d * 1.4426950408889634, -2048.0);
 }
 
+// x of the lane that CTRL names, 0 where there is none or the row is not in MASK
+template <int CTRL, int MASK>
+__device__ __forceinline__ double dpp_or_zero(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, MASK, 0xF, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, MASK, 0xF, false);
+  return __builtin_bit_cast(double, ((uint64_t)(uint32_t)hi << 32) | (uint64_t)(uint32_t)lo);
+}
+// Inclusive sums over the lanes of a wave, or of each half (L = 32): shifts within the 16-lane
+// rows, then each row's last lane added to the row (L = 64: two rows) behind it.  No LDS exchange.
+template <int L>
+__device__ __forceinline__ double lane_sums(double x) {
+  x += dpp_or_zero<0x111, 0xF>(x);  // row_shr:1
+  x += dpp_or_zero<0x112, 0xF>(x);
+  x += dpp_or_zero<0x114, 0xF>(x);
+  x += dpp_or_zero<0x118, 0xF>(x);
+  x += dpp_or_zero<0x142, 0xA>(x);  // row_bcast:15 into rows 1 and 3
+  if constexpr (L == 64) x += dpp_or_zero<0x143, 0xC>(x);  // row_bcast:31 into rows 2 and 3
+  return x;
+}
+
 // The prefix sums and step sizes of a chunk as one lane per token sees them, fetched a chunk ahead:
 // wave 0 makes R and the diagonal's parts from them, wave 1 W, wave 2 the tiles' input factors, wave
 // 3 the tiles' output factors.  Going forward the decay into p counts at p (the inclusive sums of
