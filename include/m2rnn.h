@@ -349,12 +349,15 @@ int m2rnn_gate_rmsnorm_bwd(int64_t rows, int64_t D, int io_dtype, int param_dtyp
  * (k, q, v are the layer's B, C and x; d its step size, alpha = -A its decay rate and
  * w_r = D its skip weight.)  alpha >= 0 and finite inputs are preconditions, except that
  * logit = -inf is defined: d_t = 0 and f_t = 1, the token leaves the state as it was (a
- * padding or masked token; its gradients through d_t are 0).
+ * padding or masked token; its gradients through d_t are 0).  Its k, v and q have to be
+ * finite all the same: it is multiplied by zero, not skipped.
  *
  * fp32 state: in_dtype F32 or BF16 is the type of k, v, q, y, dy, dk, dv, dq (bf16 results
  * are rounded to nearest even once); logit, alpha, beta, w_r, the states and every other
  * gradient are F32, and so are all sums.  The sizes, shared q/k heads, empty calls and
- * other conventions are those at the top of this file.
+ * other conventions are those at the top of this file; the calls over T tokens also need
+ * B * n_heads * ceil(T / 512) < 2^22, B * ceil(T / 64) * ceil(n_heads / 16) < 2^24,
+ * B * T * qk_heads * K < 2^32 and B * n_heads * K * V < 2^32 (else M2RNN_ERR_UNSUPPORTED).
  *
  * Workspace (device bytes, 16-byte aligned) of m2rnn_ssm_fwd (is_bwd = 0) or
  * m2rnn_ssm_bwd (is_bwd = 1); 0 = none.
@@ -370,7 +373,7 @@ size_t m2rnn_ssm_workspace_bytes(int is_bwd, int64_t B, int64_t T, int64_t n_hea
  *   logit  [B, T, n_heads]      in;  alpha, beta [n_heads] in;  w_r [n_heads, V] in
  *   H0     [B, n_heads, K, V]   in, or NULL for zero
  *   y      [B, T, n_heads, V]   out, in_dtype
- *   HT     [B, n_heads, K, V]   out, or NULL
+ *   HT     [B, n_heads, K, V]   out, or NULL; may be H0 itself (a state carried in place)
  */
 int m2rnn_ssm_fwd(int64_t B, int64_t T, int64_t n_heads, int64_t qk_heads, int64_t K, int64_t V,
                   int in_dtype, const void* k, const void* v, const void* q, const void* logit,
@@ -435,7 +438,8 @@ int m2rnn_ssm_step(int64_t B, int64_t n_heads, int64_t qk_heads, int64_t K, int6
  *                       hist_out (a padded batch); values outside [0, T] are taken as the nearest end
  *   out      [B, T, C]  out, io_dtype (also behind lens)
  *   hist_out [B, 3, C]  out, io_dtype, or NULL (then lens must be NULL): the last three inputs,
- *                       hist's included where there are fewer than three; T = 0 copies hist
+ *                       hist's included where there are fewer than three; T = 0 copies hist.
+ *                       May be hist itself (a history carried in place)
  */
 int m2rnn_conv_carry(int64_t B, int64_t T, int64_t C, int io_dtype, const void* x, const void* w,
                      const void* bias, const void* hist, const void* lens, void* out,

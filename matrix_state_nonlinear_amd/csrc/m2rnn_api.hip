@@ -137,16 +137,17 @@ bool newton_supported(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
   return waves < 2.0e9 && map_waves < 2.0e9 && U * (double)T * (double)K * (double)V < 4.0e18;
 }
 
-// The state-space scan's shapes: the recurrence's, and grids of fewer than 2^32 threads in
-// the backward (segments x heads, four slabs of columns at most, and one thread for each element of a
-// shared head's gradient).
+// The state-space scan's shapes: the recurrence's, and grids of fewer than 2^32 threads: the
+// sweeps' (segments of 512 tokens x heads, four slabs of columns at most), the decays' (64 tokens
+// x 16 heads), and one thread for each element of the states and of a shared head's gradient.
 bool ssm_supported(int64_t B, int64_t T, int64_t N, int64_t NQ, int64_t K, int64_t V) {
   if (!sizes_supported(B, T, N, K, V)) return false;
   if (B * T * N == 0) return true;
-  const SsmLayout L = ssm_bwd_layout(B, T, N, NQ, K, V);
-  return 4.0 * (double)B * (double)N * (double)L.nseg < (double)(1 << 24) &&
-         (double)B * (double)T * (double)NQ * (double)K < 4294967296.0 &&
-         (double)B * (double)N * (double)K * (double)V < 4294967296.0;
+  const double b = (double)B, n = (double)N;
+  return b * n * (double)((T + 511) / 512) < (double)(1 << 22) &&
+         b * (double)((T + 63) / 64) * (double)((N + 15) / 16) < (double)(1 << 24) &&
+         b * (double)T * (double)NQ * (double)K < 4294967296.0 &&
+         b * n * (double)K * (double)V < 4294967296.0;
 }
 
 // The argument checks of m2rnn_bwd and m2rnn_bwd_noalloc, before any

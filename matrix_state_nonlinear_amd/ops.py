@@ -422,6 +422,8 @@ def _given(spec, out, dev):
     """Output buffers {name: (shape, dtype), or None for one that the call does not have}: those
     given in ``out`` (None there skips dH0 and dhist), the others newly allocated."""
     given = dict(out) if out is not None else {}
+    if given.keys() - spec.keys():
+        raise ValueError(f"no outputs of this call: {sorted(given.keys() - spec.keys())}")
     o = {}
     for name, sd in spec.items():
         if name in given:
@@ -469,7 +471,8 @@ def m2rnn_ssm_fwd(k, v, q, logit, alpha, beta, w_r, H0=None, want_ht: bool = Tru
     over [B, T] tokens.  k, q [B, T, NQ, K] and v [B, T, N, V] in float32 or bfloat16 (NQ
     divides N as in m2rnn_fwd); logit [B, T, N], alpha, beta [N], w_r [N, V] and H0
     [B, N, K, V] float32.  Returns (y in v's dtype, HT float32 or None); ``out`` may hold
-    preallocated (y, HT).  logit = -inf makes a token leave the state alone."""
+    preallocated (y, HT), where HT may be H0 itself.  logit = -inf makes a token leave the state
+    alone."""
     B, T, N, NQ, K, V, io = _ssm_sizes(k, v, q, logit, alpha, beta, w_r, H0)
     dev = k.device
     if out is not None:
@@ -542,7 +545,8 @@ def m2rnn_conv_carry(x, w, bias=None, hist=None, want_hist: bool = True, lens=No
     """m2rnn_conv_silu with the three inputs before x: x [B, T, C] and hist [B, 3, C] (oldest
     first, None = zero) in float32 or bfloat16, w [C, 4] and bias [C] float32.  Returns (out
     [B, T, C], the history after x [B, 3, C] or None); ``lens`` [B] int32 says how many of each
-    sequence's inputs count for it (a padded batch).  ``out`` may hold preallocated (out, hist)."""
+    sequence's inputs count for it (a padded batch).  ``out`` may hold preallocated (out, hist),
+    where the second may be ``hist`` itself."""
     if x.dim() != 3:
         raise ValueError("x must be [B, T, C]")
     io = _io_dtype(x, "x")

@@ -69,6 +69,9 @@ def test_scan_refuses_outputs_and_workspaces(L):
         assert bwd(L, **{n: None}) == bad, n
     assert fwd(L, T=1 << 30) == E.M2RNN_ERR_UNSUPPORTED
     assert bwd(L, B=1 << 10, N=1 << 11, T=1 << 20) == E.M2RNN_ERR_UNSUPPORTED
+    # more workgroups than a launch holds, of the pass over 64 tokens x 16 heads
+    for call in (fwd, bwd):
+        assert call(L, B=1 << 11, T=1 << 19, N=1, K=1, V=1) == E.M2RNN_ERR_UNSUPPORTED
     for call, is_bwd in ((fwd, 0), (bwd, 1)):
         need = L.m2rnn_ssm_workspace_bytes(is_bwd, 2, 8, 2, 2, 16, 16, E.M2RNN_F32)
         assert need > 0
@@ -181,6 +184,8 @@ def test_binding_refuses_before_any_launch():
     with pytest.raises(ValueError, match="dH0"):
         m.m2rnn_ssm_bwd(k, v, k, x, a, a, w, None, v, want_dh0=False,
                         out={"dH0": torch.zeros(B, N, K, V)})
+    with pytest.raises(ValueError, match="no outputs.*dK"):
+        m.m2rnn_ssm_bwd(k, v, k, x, a, a, w, None, v, out={"dK": k})
     with pytest.raises(ValueError):
         m.m2rnn_ssm_step(torch.zeros(B, N, K, V), k, v, k, x, a, a, w)
     h, wc = torch.zeros(B, 3, 8), torch.zeros(8, 4)
