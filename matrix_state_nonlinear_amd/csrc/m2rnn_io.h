@@ -2,6 +2,8 @@
 // values: one access of up to 16 bytes, bf16 rounded to nearest even on the way out.
 #pragma once
 
+#include <type_traits>
+
 #include "m2rnn_device.h"
 
 namespace m2rnn {
@@ -61,6 +63,34 @@ __device__ __forceinline__ Vals<N> load(const uint16_t* p) {
   }
   return v;
 }
+// The same elements as they are stored, to be widened when they are used: registers of a load that
+// stays in flight.
+template <typename T, int N>
+struct Raw {
+  std::conditional_t<N == 1, T, std::conditional_t<N * sizeof(T) == 16, u32x4, u32x2>> r;
+  static_assert(N == 1 || N * sizeof(T) == 16 || N * sizeof(T) == 8, "");
+  __device__ __forceinline__ void load(const T* p) { r = *(const decltype(r)*)p; }
+  __device__ __forceinline__ Vals<N> vals() const {
+    Vals<N> v;
+    if constexpr (N == 1) {
+      if constexpr (sizeof(T) == 2) v.x[0] = as_float((uint32_t)r << 16);
+      else v.x[0] = r;
+    } else {
+      const auto u = r;
+#pragma unroll
+      for (int j = 0; j < (int)(N * sizeof(T) / 4); ++j) {
+        const uint32_t w = u[j];
+        if constexpr (sizeof(T) == 2) {
+          v.x[2 * j] = as_float(w << 16);
+          v.x[2 * j + 1] = as_float(w & 0xFFFF0000u);
+        } else {
+          v.x[j] = as_float(w);
+        }
+      }
+    }
+    return v;
+  }
+};
 template <int N>
 __device__ __forceinline__ void store(float* p, const Vals<N>& v) {
   if constexpr (N == 1) {
