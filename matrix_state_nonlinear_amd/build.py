@@ -15,10 +15,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libm2rnn.so")
 # the longest compiles first: they decide how long a parallel build takes
-SOURCES = ["m2rnn_ssm_sweep.hip", "m2rnn_ssm_sweep_f32.hip", "m2rnn_ssm_sweep_bf16_any.hip",
-           "m2rnn_ssm_sweep_f32_any.hip", "m2rnn_ssm.hip", "m2rnn_bwd.hip", "m2rnn_api.hip",
-           "m2rnn_gates.hip", "m2rnn_fwd.hip", "m2rnn_step.hip", "m2rnn_block.hip",
-           "m2rnn_newton.hip", "m2rnn_ssm_bwd.hip", "m2rnn_ssm_step.hip", "m2rnn_carry.hip",
+SOURCES = ["m2rnn_bwd.hip", "m2rnn_fwd.hip", "m2rnn_newton.hip", "m2rnn_ssm_sweep_f32.hip",
+           "m2rnn_ssm_sweep_f32_any.hip", "m2rnn_ssm_sweep.hip", "m2rnn_ssm_sweep_bf16_any.hip",
+           "m2rnn_ssm.hip", "m2rnn_api.hip", "m2rnn_gates.hip", "m2rnn_step.hip", "m2rnn_block.hip",
+           "m2rnn_ssm_bwd.hip", "m2rnn_ssm_step.hip", "m2rnn_carry.hip",
            "m2rnn_groupnorm.hip"]
 ARCH = "gfx950"
 

@@ -7,8 +7,9 @@
 // A head's tokens can be split into segments that run at the same time: a first pass
 // computes what each segment adds to a zero state, a scan over the segments turns these into
 // every segment's starting state, and the sweep then runs all segments from theirs.  The
-// first pass costs about half a sweep again, so T is only split as far as it takes to occupy the
-// device.
+// first pass costs almost half a sweep again, so T is only split as far as it takes to occupy the
+// device.  Four prompts of 16384 tokens, 16 heads, K = V = 64: sweep 149 us, first pass 65, decays 11,
+// scan over the segments 7.
 #include "m2rnn_ssm_sweep.h"
 
 namespace m2rnn {
@@ -44,7 +45,8 @@ hipError_t pick_at(const SsmContribArgs& a, hipStream_t stream) {
 
 // Step sizes and chunk sums of log2 f for a workgroup's 64 tokens x 16 heads: logits come in
 // rows of heads and the results go out in rows of tokens, through LDS.  A wave sums four
-// heads, a lane per token; L = 32 has two chunks to a wave.
+// heads, a lane per token; L = 32 has two chunks to a wave.  11 us for a million tokens x heads
+// (17 MB, 1.5 TB/s): the logarithm and the double sums bound it, not the memory.
 template <int L>
 __global__ void __launch_bounds__(256)
     m2rnn_ssm_decays_kernel(int64_t T, int64_t N, const float* __restrict__ logit,
@@ -80,7 +82,8 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// One thread per state element; blockIdx.y the scan.  Loads run four segments ahead of the sums.
+// One thread per state element; blockIdx.y the scan.  Loads run four segments ahead of the sums: 7 us
+// for 12 segments of 64 heads of 64 x 64 states (25 MB, each read and written; a launch's latency).
 __global__ void __launch_bounds__(256)
     m2rnn_ssm_segscan_kernel(const SsmSegScans scans, const float* __restrict__ fseg, int64_t total,
                              int64_t nseg, int64_t KV) {
@@ -127,12 +130,14 @@ hipError_t launch_ssm_segscan(const SsmSegScans& scans, const float* fseg, int64
   return hipGetLastError();
 }
 
-// Workgroups of the forward's sweep that a CU holds (m2rnn_ssm_sweep.h).
+// Workgroups of the forward's sweep that a CU holds (LDS and registers of m2rnn_ssm_sweep.h).
 int64_t ssm_per_cu(int64_t K, int64_t V, int in_dtype) {
   return in_dtype == kBF16 && K <= 64 && V <= 64 ? 3 : 2;
 }
 
-// Segments of the forward: as many as fill every CU once, of at least 64 tokens.
+// Segments of the forward: as many as fill every CU once, of at least 64 tokens.  Four prompts of
+// 16384 tokens, 16 heads, K = V = 64: 236 us (12 segments); unsplit 884 us, 24 segments 246.  One of
+// 2048 tokens: 35 us, unsplit 109.
 SsmLayout ssm_fwd_layout(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V, int in_dtype) {
   SsmLayout L{};
   const int64_t units = B * N, wgs = units * ssm_slabs(K, V);

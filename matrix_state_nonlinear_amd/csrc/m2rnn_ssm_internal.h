@@ -98,8 +98,10 @@ struct SsmArgs {
 };
 
 // Columns of the output (DC of the sweep, contracting over DA) per workgroup: up to 128, or 64
-// where a 128-column state would not leave registers for two workgroups per CU (one prompt of
-// 16384 tokens, 32 heads, K = V = 128: the sweep takes 230 us with 128 columns, 225 us with 64).
+// where a 128-column state would not leave registers for two workgroups per CU.  Four prompts of
+// 4096 tokens, 16 heads, K = 64, V = 128: 94 us with 128 columns, 106 with 64 (each slab reads the
+// other tensors again); one of 16384 tokens, 32 heads, K = V = 128: the sweep takes 230 us with 128
+// columns, 213 with 64.
 inline int ssm_columns(int64_t DA, int64_t DC) { return DC > 64 && DA <= 64 ? 128 : 64; }
 inline int64_t ssm_slabs(int64_t DA, int64_t DC) {
   const int c = ssm_columns(DA, DC);
@@ -133,7 +135,8 @@ hipError_t launch_ssm_contrib(const SsmContribArgs& a, int in_dtype, hipStream_t
 hipError_t launch_ssm_decays(const SsmArgs& a, int in_dtype, double* cum, float* d,
                              hipStream_t stream);
 // Whether rows of `heads` x `D` elements at p can be accessed in 16-byte pieces with 32-bit offsets
-// within a chunk.
+// within a chunk.  Element accesses otherwise (670 us instead of 234 for four prompts of 16384
+// tokens, 16 heads, K = V = 64).
 bool ssm_vec_rows(const void* p, int64_t heads, int64_t D, int elem_bytes);
 // Scans over the segments, one or two in a launch: seg [units, nseg, KV] (what a segment adds)
 // becomes the state each starts from (rev: ends at), `first` [units, KV] or null = 0 the first

@@ -2,8 +2,10 @@
 //     d = softplus(logit + beta),  H <- exp(-alpha d) H + d k v^T,  y = H^T q + w_r (.) v.
 // The state is read and written once, 8 K V bytes a head against 4 K V multiply-adds, so the
 // step is bound by HBM.  A wave (W = 1) or a workgroup of four takes a head: lanes run along V in
-// 16-byte pieces and then along K, eight pieces per lane in flight; the columns' sums are
-// joined by lane exchanges and, for four waves, through LDS.
+// 16-byte pieces and then along K, four pieces per lane in flight; the columns' sums are
+// joined by lane exchanges and, for four waves, through LDS.  512 sequences of 16 heads, K = V = 64:
+// 46 us for 273 MB (5.9 TB/s, part of the state still in the memory-side cache from the step
+// before; 62 us after other work has emptied it, 4.4 TB/s); sixteen pieces in flight took 87.
 #include "m2rnn_io.h"
 #include "m2rnn_ssm_internal.h"
 #include "m2rnn_ssm_sweep.h"
@@ -133,9 +135,11 @@ hipError_t run(SsmStepArgs g, bool vec, hipStream_t stream) {
 
 hipError_t launch_ssm_step(const SsmStepArgs& g, int in_dtype, hipStream_t stream) {
   const bool vec = g.V % 4 == 0 && aligned16(g.H);
-  // a wave holds 4 x 64 x 4 elements in flight: larger heads are shared by four waves, and so are
-  // the heads of calls that would leave most CUs without a wave
-  const bool split = g.K * g.V > 4096 || (g.B * g.N < 512 && g.K * g.V >= 1024);
+  // a wave holds 4 x 64 x 4 elements in flight: larger heads are shared by four waves (8192 heads of
+  // 64 x 64: 45.8 us shared, 48.0 not; of 2048, 128 x 128: 45 and 60; but 32768 of 64 x 16: 84 and
+  // 48), and so are the heads of calls that would leave most CUs without a wave (64 of 64 x 16: 13.3 us
+  // and 14.1 with the call)
+  const bool split = g.K * g.V >= 4096 || (g.B * g.N < 512 && g.K * g.V >= 1024);
   if (in_dtype == kBF16)
     return split ? run<uint16_t, 4>(g, vec, stream) : run<uint16_t, 1>(g, vec, stream);
   return split ? run<float, 4>(g, vec, stream) : run<float, 1>(g, vec, stream);

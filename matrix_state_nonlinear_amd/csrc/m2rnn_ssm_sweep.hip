@@ -24,8 +24,10 @@ hipError_t run(const SsmSweepArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Columns per workgroup (ssm_columns), and how many waves share them when there are few; dq
-// contracts over them in blocks of 32.
+// Columns per workgroup (ssm_columns), and how many waves share them when there are few: two or
+// four waves split the chunk's rows instead of repeating them (two prompts of 4096 tokens, 64 heads
+// on one q and k, K = 64: V = 16 takes 74 us shared and 86 not; four of 8192, 16 heads, V = 32 84
+// and 92); dq contracts over the columns in blocks of 32, so four would have nothing to share.
 template <typename InT, int AT, int MODE>
 hipError_t pick_nt(const SsmSweepArgs& a, hipStream_t stream) {
   if constexpr (AT <= 2)
