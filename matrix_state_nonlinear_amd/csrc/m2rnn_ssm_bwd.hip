@@ -4,13 +4,15 @@
 // The sweeps return, per token, the parts of the decays' gradient inside a chunk (X_t, the sum of
 // M over the pairs around t) and those of the carried states (a_t, b_t; m2rnn_ssm_sweep.h has
 // the definitions).  The part g = 2^{c_L} <H0, G> that passes through the whole chunk follows from
-// w = <state, state gradient> at the chunk's end, w_end = sum b + g, and gives the next one,
-// w_start = sum a + g; the first w is a dot product at the segment's end.  Then
+// w = <state, state gradient> at the chunk's end, w_end = sum b + g, or its start, w_start = sum a +
+// g: from the segment's end, where w is a dot product, backwards, and from its start, the end of
+// the segment before, forwards.  Each chunk adds the rounding of its sums to the one and the other;
+// g is their mean weighted against that (dalpha 3.0e-6 off from the end alone, 1.2e-6 so).  Then
 //     dl_t = X_t + sum_{i >= t} a_i + sum_{j < t} b_j + g,
 //     dlogit = sigmoid(x) (dd - alpha dl),  d dd = sum_i M_it + b_t.
 // These sums are kept in double.  Where the chunk's decay is below kNoPass, g is below what
 // w_end - sum b is rounded by, and is left out: the difference would add the same error to all the
-// chunk's tokens (with it dalpha at B = 16, T = 4096, 16 heads was 7e-6 off, without it 3e-6).
+// chunk's tokens (with it dalpha at B = 16, T = 4096, 16 heads was more than twice as far off).
 //
 // B = 16, T = 4096, 16 heads, K = 32, V = 128, bf16 (the whole backward 960 us): decays 12 us, the
 // states' two first passes 80 us each, their scans 15, dq 302, dv 227, dk 252, the decays' gradient 28,
@@ -22,8 +24,8 @@ namespace m2rnn {
 namespace {
 
 // Tokens per segment at most: the decays' gradient carries w from chunk to chunk inside a segment,
-// and its error with it (at B = 16, T = 4096, 16 heads, K = 32, V = 128 dbeta is 6e-7 off with
-// 512 and 1.2e-6 with 1024; the whole training call takes 1.18 and 1.13 ms).
+// and its error with it (at B = 16, T = 4096, 16 heads, K = 32, V = 128 dalpha and dbeta are 1.2e-6
+// and 3e-7 off with 512, 2.5e-6 and 8e-7 with 1024; forward and backward take 1.19 and 1.13 ms).
 constexpr int64_t kMaxSeg = 512;
 constexpr int kMaxChunks = 16;  // of 32 tokens
 constexpr double kNoPass = 15.0;  // -log of 3e-7
@@ -38,10 +40,10 @@ __global__ void __launch_bounds__(64 * kMaxChunks)
     m2rnn_ssm_dgate_kernel(int64_t B, int64_t T, int64_t N, int64_t nseg, int64_t seglen, int L,
                            int slabs, int vslabs, const float* __restrict__ adot,
                            const float* __restrict__ bdot, const float* __restrict__ pairs,
-                           const float* __restrict__ colpairs, const float* __restrict__ base,
-                           const float* __restrict__ logit, const float* __restrict__ alpha,
-                           const float* __restrict__ beta, float* __restrict__ dlogit,
-                           float* __restrict__ part) {
+                           const float* __restrict__ colpairs, const double* __restrict__ base,
+                           bool from_zero, const float* __restrict__ logit,
+                           const float* __restrict__ alpha, const float* __restrict__ beta,
+                           float* __restrict__ dlogit, float* __restrict__ part) {
   __shared__ double tot[3][kMaxChunks];  // per chunk: sums of a and b, and its -log f in all
   __shared__ double red[2][kMaxChunks];
   // heads fastest: neighbouring workgroups share lines of logit and dlogit
@@ -88,12 +90,24 @@ __global__ void __launch_bounds__(64 * kMaxChunks)
   if (lane == 63) tot[0][w] = asum;
   bsum -= b_own;
   __syncthreads();
-  double w_end = 0.0, g = 0.0;
+  double w_end = 0.0, w_start = 0.0, g = 0.0, g_left = 0.0;
   if (base)
-    for (int s = 0; s < vslabs; ++s) w_end += (double)base[((int64_t)s * B * N + bn) * nseg + seg];
+    for (int s = 0; s < vslabs; ++s) {
+      const double* p = base + ((int64_t)s * B * N + bn) * nseg + seg;
+      w_end += p[0];
+      if (seg > 0) w_start += p[-1];
+    }
   for (int k = nch - 1; k >= w; --k) {
     g = tot[2][k] > kNoPass ? 0.0 : w_end - tot[1][k];
     w_end = tot[0][k] + g;
+  }
+  if (seg > 0 || from_zero) {  // (w at the first token's start is not known with an initial state)
+    for (int k = 0; k <= w; ++k) {
+      g_left = tot[2][k] > kNoPass ? 0.0 : w_start - tot[0][k];
+      w_start = tot[1][k] + g_left;
+    }
+    const double share = ((double)w + 0.5) / (double)nch;
+    g = g * share + g_left * (1.0 - share);
   }
   double sa = 0.0, sb = 0.0;
   if (ok) {
@@ -199,7 +213,7 @@ SsmLayout ssm_bwd_layout(int64_t B, int64_t T, int64_t N, int64_t NQ, int64_t K,
   L.gseg = take(U * L.nseg * KV);
   L.hT = take(U * KV);
   L.fseg = take(U * L.nseg);
-  L.base = take(U * L.nseg * ssm_slabs(K, V));
+  L.base = take(U * L.nseg * ssm_slabs(K, V) * 2);
   L.adot = take(U * T * ssm_slabs(V, K));
   L.bdot = take(U * T * ssm_slabs(V, K));
   L.pairs = take(U * T * ssm_slabs(V, K));
@@ -284,7 +298,7 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
   dv.state0 = passes ? gseg : nullptr;
   dv.stateT = passes ? nullptr : a.dH0;
   if (passes) {
-    dv.base = a.ws + L.base;
+    dv.base = (double*)(a.ws + L.base);
     dv.hend = hseg;
     dv.hend_last = hT;
   }
@@ -313,7 +327,7 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
                      dim3((unsigned)(64 * ceil_div(L.seglen, chunk))), 0, stream, a.B, a.T, a.N,
                      L.nseg, L.seglen, chunk, (int)ssm_slabs(a.V, a.K), (int)ssm_slabs(a.K, a.V),
                      a.ws + L.adot, a.ws + L.bdot, a.ws + L.pairs, a.ws + L.colpairs,
-                     passes ? a.ws + L.base : nullptr, a.logit, a.alpha, a.beta, a.dlogit,
+                     passes ? (const double*)(a.ws + L.base) : nullptr, a.H0 == nullptr, a.logit, a.alpha, a.beta, a.dlogit,
                      a.ws + L.gatepart);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   hipLaunchKernelGGL(m2rnn_ssm_params_kernel, dim3((unsigned)(a.N * ceil_div(a.V + 2, 64))),

@@ -29,7 +29,7 @@ struct SsmSweepArgs {
   const float* hend;    // base only: [B, N, nseg, *], the other state at each segment's end is
                         // entry s + 1, and hend_last [B, N, *] for the last one
   const float* hend_last;
-  float* base;          // [slabs, B, N, nseg] or null: <state0, hend> of every segment
+  double* base;         // [slabs, B, N, nseg] or null: <state0, hend> of every segment
   int64_t B, T, N, nseg, seglen, slabs;
   int a_grp, b_grp, c_grp, e_grp;
   int DA, DC;

@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, MODE, sizeof(InT)
       lds_barrier();
       if (threadIdx.x == 0)
         g.base[((int64_t)slab * g.B * g.N + bn) * g.nseg + seg] =
-            (float)((red[0] + red[1]) + (red[2] + red[3]));
+            (red[0] + red[1]) + (red[2] + red[3]);
       lds_barrier();
     }
   }
