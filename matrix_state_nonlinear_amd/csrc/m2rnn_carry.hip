@@ -9,7 +9,7 @@
 #include <type_traits>
 
 #include "m2rnn_io.h"
-#include "m2rnn_internal.h"
+#include "m2rnn_serving_internal.h"
 
 namespace m2rnn {
 

@@ -10,7 +10,7 @@
 // of 64 channels in bf16: forward 86 us (403 MB, 4.7 TB/s), backward 136 us (671 MB, 4.9 TB/s; a copy
 // reaches 5.2) and 7 us for the partials; 512 rows 4 us.
 #include "m2rnn_io.h"
-#include "m2rnn_internal.h"
+#include "m2rnn_serving_internal.h"
 
 namespace m2rnn {
 
