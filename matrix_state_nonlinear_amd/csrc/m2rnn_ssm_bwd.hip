@@ -14,9 +14,9 @@
 // w_end - sum b is rounded by, and is left out: the difference would add the same error to all the
 // chunk's tokens (with it dalpha at B = 16, T = 4096, 16 heads was more than twice as far off).
 //
-// B = 16, T = 4096, 16 heads, K = 32, V = 128, bf16 (the whole backward 960 us): decays 12 us, the
-// states' two first passes 80 us each, their scans 15, dq 302, dv 227, dk 252, the decays' gradient 28,
-// parameters 13.
+// B = 16, T = 4096, 16 heads, K = 32, V = 128, bf16: the call takes 0.9 ms; under the profiler, which
+// stretches them by a tenth, decays 12 us, the states' two first passes 82 and 84, their scans 28, dq 315,
+// dv 244, dk 264, the decays' gradient 27, parameters 15.
 #include "m2rnn_ssm_sweep.h"
 
 namespace m2rnn {
@@ -35,7 +35,7 @@ size_t pad64(size_t x) { return align_up(x, 64); }
 
 // One workgroup per (b, n, segment), a wave per chunk of `L` tokens (as in the sweeps): the sums
 // inside the chunks all at once, then every wave follows w from the segment's end to its chunk.
-// Bound by the latency of its few loads per thread (28 us for 25 MB at the size above).
+// Bound by the latency of its few loads per thread (27 us for 25 MB at the size above).
 __global__ void __launch_bounds__(64 * kMaxChunks)
     m2rnn_ssm_dgate_kernel(int64_t B, int64_t T, int64_t N, int64_t nseg, int64_t seglen, int L,
                            int slabs, int vslabs, const float* __restrict__ adot,

@@ -36,10 +36,10 @@
 //
 // What bounds it.  A token and head takes about 2 L (DA + DC) + 4 DA DC operations in chunks of L
 // tokens, far below the matrix cores' rate for the bytes it reads: the forward sweep is bound by how
-// fast the tiles come in.  Four prompts of 16384 tokens, 16 heads, K = V = 64, bf16: 149 us for 549 MB
-// (3.7 TB/s; the same kernel without its products took nine tenths of that; a copy reaches 5.2 TB/s
-// on rows that lie together, these are 128 bytes every 2 KB).  The dq and dk sweeps (302 and 252 us
-// at B = 16, T = 4096, 16 heads, K = 32, V = 128, 750 MB each) also issue on 55 to 65 % of the
+// fast the tiles come in.  Four prompts of 16384 tokens, 16 heads, K = V = 64, bf16: 144 us for 562 MB
+// (3.9 TB/s; the same kernel without its products took nine tenths of that; a copy reaches 5.2 TB/s
+// on rows that lie together, these are 128 bytes every 2 KB).  The dq and dk sweeps (315 and 264 us
+// at B = 16, T = 4096, 16 heads, K = 32, V = 128, 800 MB each) also issue on 52 to 57 % of the
 // cycles: two score products, the pair sums and the splits.  Loads run a chunk ahead in registers and cross
 // the barriers (lds_barrier); with __syncthreads and branches around them the prompt took 311 us.
 #pragma once
@@ -1016,7 +1016,7 @@ __global__ void __launch_bounds__(256, sweep_occupancy(AT, NT, MODE, sizeof(InT)
 // The state a segment adds to a zero start: the sweep's state update alone.  Both directions
 // walk from the segment's last chunk to its first: with forward decays a chunk's inputs are
 // weighted by all that follows (`run`), and the sweep that comes next, walking forward, finds
-// the tokens read last in the memory-side cache.  65 us for 270 MB (4.1 TB/s) at the prompt above:
+// the tokens read last in the memory-side cache.  66 us for 294 MB (4.5 TB/s) at the prompt above:
 // bound by the loads, two products a chunk against the sweep's five.  One workgroup per CU for wide
 // states and fp32 ones, whose registers would spill with two.
 template <typename InT, int AT, int NT, int RS, bool REV, bool VEC>
