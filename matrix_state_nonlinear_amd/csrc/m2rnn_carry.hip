@@ -1,11 +1,13 @@
 // The short causal convolution with a history that is carried between calls (prompts in
 // pieces, truncated training windows, single tokens):
 //     u_t[c] = bias[c] + sum_{i<4} w[c][i] x_{t-3+i}[c],  out = SiLU(u),  x_{-3..-1} = hist.
-// All kernels are bound by HBM: threads take 16 bytes of consecutive channels (one element
-// where C or an address does not allow it), slide the last inputs through registers over a run of
-// time steps, and read and write each tensor once (runs overlap by three steps, the backward's by
-// six).  At B = 4, T = 16384, C = 1024 in bf16 the forward takes 58 us (268 MB, 4.6 TB/s) and the
-// backward 84 us (403 MB, 4.8 TB/s; a copy reaches 5.2); one token of 512 sequences 5 us.
+// All kernels are bound by HBM: threads take four consecutive channels (one where C or an address
+// does not allow it), slide the last inputs through registers over a run of time steps, fetch them a
+// group of steps ahead, and read and write each tensor once (runs overlap by three steps, the
+// backward's by six).  At B = 4, T = 16384, C = 1024 in bf16 the forward takes 50 us (268 MB, 5.3
+// TB/s, what a copy reaches) and the backward 84 us (403 MB, 4.8 TB/s); one token of 512 sequences 4 us.
+// Eight channels (16 bytes of bf16) took 56 us forward, 104 backward and 4.7 us for the token: taps,
+// sums and sliding inputs take up to 24 registers a channel, and half the waves are there to wait.
 #include <type_traits>
 
 #include "m2rnn_io.h"
@@ -17,7 +19,7 @@ namespace {
 
 constexpr int kRunFwd = 16;  // time steps per thread, forward
 constexpr int kRunBwd = 32;  // and backward
-constexpr int kGroup = 4;    // of them fetched at a time, backward
+constexpr int kGroup = 4;    // of them fetched at a time
 constexpr int kRunsPerGroup = 4;  // runs (one per wave) whose sums a backward workgroup joins
 
 template <int VEC>
@@ -48,6 +50,8 @@ __device__ __forceinline__ io::Vals<VEC> at(const IoT* x, const IoT* hist, int64
   return z;
 }
 
+// A wave per run of 16 steps and 256 channels.  Runs of 32 take 49 us at the size above, but 9.3
+// instead of 6.9 at B = 1, T = 4096; without the fetch a group ahead 58 and 11.
 template <typename IoT, int VEC>
 __global__ void __launch_bounds__(256) m2rnn_conv_carry_kernel(const CarryArgs g, int64_t runs) {
   const int64_t Cv = g.C / VEC, cblocks = (Cv + 63) / 64;
@@ -65,9 +69,7 @@ __global__ void __launch_bounds__(256) m2rnn_conv_carry_kernel(const CarryArgs g
   IoT* out = (IoT*)g.out + b * g.T * g.C + c;
   io::Vals<VEC> m3 = at<IoT, VEC>(x, hist, t0 - 3, g.C), m2 = at<IoT, VEC>(x, hist, t0 - 2, g.C),
                 m1 = at<IoT, VEC>(x, hist, t0 - 1, g.C);
-#pragma unroll 8
-  for (int64_t t = t0; t < t1; ++t) {
-    const io::Vals<VEC> xt = io::load<VEC>(x + t * g.C);
+  auto step = [&](int64_t t, const io::Vals<VEC>& xt) {
     io::Vals<VEC> o;
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
@@ -78,7 +80,26 @@ __global__ void __launch_bounds__(256) m2rnn_conv_carry_kernel(const CarryArgs g
     m3 = m2;
     m2 = m1;
     m1 = xt;
+  };
+  // groups of steps, fetched one group ahead, without branches (a load in a branch would be waited
+  // for at its end; rows past the sequence's end are its last row's)
+  const int64_t last = g.T - 1;
+  io::Raw<IoT, VEC> xr[kGroup];
+  auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) xr[i].load(x + (t + i < last ? t + i : last) * g.C);
+  };
+  fetch(t0);
+  int64_t t = t0;
+  for (; t + kGroup <= t1; t += kGroup) {
+    io::Vals<VEC> xv[kGroup];
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) xv[i] = xr[i].vals();
+    fetch(t + kGroup);
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) step(t + i, xv[i]);
   }
+  for (; t < t1; ++t) step(t, io::load<VEC>(x + t * g.C));
   if (g.hist_out && t0 == 0) {  // the last three inputs of the first len ones (bf16 widens and
                                 // rounds back exactly)
     int64_t len = g.lens ? (int64_t)g.lens[b] : g.T;
@@ -91,10 +112,9 @@ __global__ void __launch_bounds__(256) m2rnn_conv_carry_kernel(const CarryArgs g
 
 // du_t = dout_t SiLU'(u_t) for the run and the three steps after it; dx_s = sum_i w[i] du_{s+3-i}
 // follows three steps behind.  The run that starts a sequence also gives dhist (s < 0).  Sums of
-// du_t x_{t-3+i} and du_t over the four waves' runs go to part[group][5][C].  Four channels per
-// thread in both types: taps, sums and the sliding inputs take 24 registers a channel, so eight
-// leave one wave per SIMD (104 us at the size above, 84 with four).  Runs of 64 steps instead
-// of 32 took 90 us there and 23 instead of 16 at B = 1, T = 4096; without the fetch a group ahead 114.
+// du_t x_{t-3+i} and du_t over the four waves' runs go to part[group][5][C].  Runs of 64 steps instead
+// of 32 take 90 us at the size above and 23 instead of 16 at B = 1, T = 4096; without the fetch a
+// group ahead (and with eight channels) it was 114.
 template <typename IoT, int VEC>
 __global__ void __launch_bounds__(256)
     m2rnn_conv_carry_bwd_kernel(const CarryArgs g, int64_t runs, float* __restrict__ part) {
@@ -168,8 +188,7 @@ __global__ void __launch_bounds__(256)
     using Yes = std::true_type;
     using No = std::false_type;
     static_assert(kGroup >= 3, "the first group holds all steps whose dx is not the run's");
-    // groups of kGroup steps, fetched one group ahead (without branches: a load in a branch would be
-    // waited for at its end; rows past the sequence's end are its last row's)
+    // groups of steps, fetched one group ahead as in the forward
     const int64_t last = g.T - 1;
     io::Raw<IoT, VEC> xr[kGroup], gr[kGroup];
     auto fetch = [&](int64_t t) {
@@ -292,22 +311,16 @@ hipError_t one(const CarryArgs& g, hipStream_t stream) {
                      dim3((unsigned)ceil_div(g.B * (g.C / VEC), 256)), dim3(256), 0, stream, g);
   return hipGetLastError();
 }
-// Whether every tensor can be accessed in pieces of `bytes`, `n` elements each.
-bool pieces_ok(const CarryArgs& g, int n, uintptr_t bytes) {
+template <typename IoT>
+hipError_t pick(const CarryArgs& g, int what, hipStream_t stream) {
   uintptr_t all = 0;
   for (const void* p : {g.x, g.hist, (const void*)g.out, (const void*)g.hist_out, g.dout,
                         (const void*)g.dx, (const void*)g.dhist})
     all |= (uintptr_t)p;
-  return g.C % n == 0 && all % bytes == 0;
-}
-template <typename IoT>
-hipError_t pick(const CarryArgs& g, int what, hipStream_t stream) {
-  constexpr int N = io::kVec<IoT>;
-  if (what == 1)
-    return pieces_ok(g, 4, 4 * sizeof(IoT)) ? bwd<IoT, 4>(g, stream) : bwd<IoT, 1>(g, stream);
-  const bool vec = pieces_ok(g, N, 16);
-  if (what == 0) return vec ? fwd<IoT, N>(g, stream) : fwd<IoT, 1>(g, stream);
-  return vec ? one<IoT, N>(g, stream) : one<IoT, 1>(g, stream);
+  const bool vec = g.C % 4 == 0 && all % (4 * sizeof(IoT)) == 0;
+  if (what == 0) return vec ? fwd<IoT, 4>(g, stream) : fwd<IoT, 1>(g, stream);
+  if (what == 1) return vec ? bwd<IoT, 4>(g, stream) : bwd<IoT, 1>(g, stream);
+  return vec ? one<IoT, 4>(g, stream) : one<IoT, 1>(g, stream);
 }
 
 }  // namespace
