@@ -357,7 +357,8 @@ int m2rnn_gate_rmsnorm_bwd(int64_t rows, int64_t D, int io_dtype, int param_dtyp
  * gradient are F32, and so are all sums.  The sizes, shared q/k heads, empty calls and
  * other conventions are those at the top of this file; the calls over T tokens also need
  * B * n_heads * ceil(T / 512) < 2^22, B * ceil(T / 64) * ceil(n_heads / 16) < 2^24,
- * B * T * qk_heads * K < 2^32 and B * n_heads * K * V < 2^32 (else M2RNN_ERR_UNSUPPORTED).
+ * n_heads * (V + 65) < 2^28, B * T * qk_heads * K < 2^32 and B * n_heads * K * V < 2^32
+ * (else M2RNN_ERR_UNSUPPORTED).
  *
  * Workspace (device bytes, 16-byte aligned) of m2rnn_ssm_fwd (is_bwd = 0) or
  * m2rnn_ssm_bwd (is_bwd = 1); 0 = none.

@@ -140,13 +140,15 @@ bool newton_supported(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
 
 // The state-space scan's shapes: the recurrence's, and grids of fewer than 2^32 threads: the
 // sweeps' (segments of 512 tokens x heads, four slabs of columns at most), the decays' (64 tokens
-// x 16 heads), and one thread for each element of the states and of a shared head's gradient.
+// x 16 heads), the parameters' (heads x 64 columns, 1024 threads each), and one thread for each
+// element of the states and of a shared head's gradient.
 bool ssm_supported(int64_t B, int64_t T, int64_t N, int64_t NQ, int64_t K, int64_t V) {
   if (!sizes_supported(B, T, N, K, V)) return false;
   if (B * T * N == 0) return true;
   const double b = (double)B, n = (double)N;
   return b * n * (double)((T + 511) / 512) < (double)(1 << 22) &&
          b * (double)((T + 63) / 64) * (double)((N + 15) / 16) < (double)(1 << 24) &&
+         n * ((double)V + 65.0) < (double)(1 << 28) &&
          b * (double)T * (double)NQ * (double)K < 4294967296.0 &&
          b * n * (double)K * (double)V < 4294967296.0;
 }

@@ -16,7 +16,7 @@
 //
 // B = 16, T = 4096, 16 heads, K = 32, V = 128, bf16: the call takes 0.9 ms; under the profiler, which
 // stretches them by a tenth, decays 12 us, the states' two first passes 82 and 84, their scans 28, dq 315,
-// dv 244, dk 264, the decays' gradient 27, parameters 15.
+// dv 244, dk 264, the decays' gradient 27, parameters 7.
 #include "m2rnn_ssm_sweep.h"
 
 namespace m2rnn {
@@ -136,14 +136,15 @@ __global__ void __launch_bounds__(64 * kMaxChunks)
 }
 
 // dw_r[n][x] = sum over (b, segment) of colsum[b][n][seg][x], x < V, and dalpha, dbeta from
-// part[b][n][seg][2] as columns V and V + 1.  64 columns of a head per workgroup, its four
-// waves taking every fourth (b, segment), joined in a fixed order.
-__global__ void __launch_bounds__(256)
+// part[b][n][seg][2] as columns V and V + 1.  64 columns of a head per workgroup, its sixteen
+// waves taking every sixteenth (b, segment), joined in a fixed order (7 us for 16 heads of 128
+// (b, segment); with four waves 15).
+__global__ void __launch_bounds__(1024)
     m2rnn_ssm_params_kernel(int64_t B, int64_t N, int64_t nseg, int64_t V,
                             const float* __restrict__ colsum, const float* __restrict__ part,
                             float* __restrict__ dw_r, float* __restrict__ dalpha,
                             float* __restrict__ dbeta) {
-  __shared__ double red[4][64];
+  __shared__ double red[16][64];
   const int64_t cb = (V + 2 + 63) / 64;
   const int64_t n = blockIdx.x / cb;
   const int64_t x = (blockIdx.x % cb) * 64 + (threadIdx.x & 63);
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(256)
   double sum = 0.0;
   if (x < V + 2) {
 #pragma unroll 4
-    for (int64_t r = grp; r < B * nseg; r += 4) {
+    for (int64_t r = grp; r < B * nseg; r += 16) {
       const int64_t row = (r / nseg * N + n) * nseg + r % nseg;
       sum += (double)(x < V ? colsum[row * V + x] : part[row * 2 + (x - V)]);
     }
@@ -159,8 +160,10 @@ __global__ void __launch_bounds__(256)
   red[grp][threadIdx.x & 63] = sum;
   __syncthreads();
   if (grp != 0 || x >= V + 2) return;
-  const int l = threadIdx.x;
-  const float total = (float)((red[0][l] + red[1][l]) + (red[2][l] + red[3][l]));
+  double all = 0.0;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) all += red[k][threadIdx.x];
+  const float total = (float)all;
   if (x < V) dw_r[n * V + x] = total;
   else if (x == V) dalpha[n] = total;
   else dbeta[n] = total;
@@ -327,11 +330,11 @@ hipError_t launch_ssm_bwd(const SsmArgs& a, int in_dtype, hipStream_t stream) {
                      dim3((unsigned)(64 * ceil_div(L.seglen, chunk))), 0, stream, a.B, a.T, a.N,
                      L.nseg, L.seglen, chunk, (int)ssm_slabs(a.V, a.K), (int)ssm_slabs(a.K, a.V),
                      a.ws + L.adot, a.ws + L.bdot, a.ws + L.pairs, a.ws + L.colpairs,
-                     passes ? (const double*)(a.ws + L.base) : nullptr, a.H0 == nullptr, a.logit, a.alpha, a.beta, a.dlogit,
-                     a.ws + L.gatepart);
+                     passes ? (const double*)(a.ws + L.base) : nullptr, a.H0 == nullptr, a.logit,
+                     a.alpha, a.beta, a.dlogit, a.ws + L.gatepart);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   hipLaunchKernelGGL(m2rnn_ssm_params_kernel, dim3((unsigned)(a.N * ceil_div(a.V + 2, 64))),
-                     dim3(256), 0, stream, a.B, a.N, L.nseg, a.V, a.ws + L.colsum,
+                     dim3(1024), 0, stream, a.B, a.N, L.nseg, a.V, a.ws + L.colsum,
                      a.ws + L.gatepart, a.dw_r, a.dalpha, a.dbeta);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   if (grp > 1) {

@@ -72,6 +72,8 @@ def test_scan_refuses_outputs_and_workspaces(L):
     # more workgroups than a launch holds, of the pass over 64 tokens x 16 heads
     for call in (fwd, bwd):
         assert call(L, B=1 << 11, T=1 << 19, N=1, K=1, V=1) == E.M2RNN_ERR_UNSUPPORTED
+        # and of the sums over heads x 64 columns
+        assert call(L, B=1, T=8, N=1 << 21, K=1, V=128) == E.M2RNN_ERR_UNSUPPORTED
     for call, is_bwd in ((fwd, 0), (bwd, 1)):
         need = L.m2rnn_ssm_workspace_bytes(is_bwd, 2, 8, 2, 2, 16, 16, E.M2RNN_F32)
         assert need > 0
