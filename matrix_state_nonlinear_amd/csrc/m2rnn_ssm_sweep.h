@@ -557,7 +557,7 @@ constexpr int sweep_occupancy(int AT, int NT, int mode, int bytes) {  // AT * NT
   return AT == 8 || (bytes == 4 && mode == kDq && AT * NT >= 4) ? 1 : 2;
 }
 
-// KEEP: the state is kept to 24 bits (it is an output, or goes into the decays' gradient); one that
+// KEEP: the state is kept to 24 bits (it may be an output, or goes into the decays' gradient); one that
 // only goes into bf16 outputs takes its inputs in two terms, like its readout (234 us for the prompt
 // above with its passes; with three terms 247).
 template <typename InT, int AT, int NT, int RS, int MODE, bool KEEP, bool VEC>
@@ -1125,7 +1125,8 @@ __global__ void __launch_bounds__(256, (AT * NT <= 4 && sizeof(InT) == 2) ? 2 : 
         bf16x8 xb[P];
 #pragma unroll
         for (int p = 0; p < P; ++p)
-          xb[p] = col8(sh.b + p * TB::PLANE + (32 * jb + 8 * q4) * TB::STRIDE + 16 * (HA * rg + at), TB::STRIDE, m);
+          xb[p] = col8(sh.b + p * TB::PLANE + (32 * jb + 8 * q4) * TB::STRIDE +
+                           16 * (HA * rg + at), TB::STRIDE, m);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) st[at][nt] = mfma_terms(xb, cw[nt], st[at][nt]);
       }

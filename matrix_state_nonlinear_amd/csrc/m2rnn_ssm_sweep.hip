@@ -14,7 +14,8 @@ template <typename InT, int AT, int NT, int RS, int MODE>
 hipError_t run(const SsmSweepArgs& a, hipStream_t stream) {
   const dim3 grid((unsigned)(a.B * a.N * a.nseg * a.slabs));
   if constexpr (sizeof(InT) == 2 && (MODE == ssm::kY || MODE == ssm::kDv))
-    if (!a.stateT) {
+    if (a.nseg > 1) {  // the last state comes from the segments' scan (asked for or not, so that the
+                       // other results do not depend on it)
       hipLaunchKernelGGL((ssm::m2rnn_ssm_sweep_kernel<InT, AT, NT, RS, MODE, false, M2RNN_SSM_VEC>),
                          grid, dim3(256), 0, stream, a);
       return hipGetLastError();

@@ -117,3 +117,49 @@ def test_norm_backward_of_one_row_twice():
         assert torch.equal(two[i][:5], one[i]) and torch.equal(two[i][5:], one[i])
     for i in (2, 3):  # ten terms of order 1, in another order
         assert np.allclose(two[i].cpu(), 2 * one[i].cpu(), rtol=0, atol=2.0 ** -19 * 10)
+
+
+# one segment per head and several
+SPLITS = [(65, 70, 8, 16, 16), (2, 500, 2, 40, 72)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,T,N,K,V", SPLITS)
+@pytest.mark.parametrize("given", ["H0", "dHT"])
+def test_backward_with_one_of_the_states(given, B, T, N, K, V, dtype):
+    h, d = inputs(B, T, N, 1, K, V, dtype, seed=T)
+    other = "dHT" if given == "H0" else "H0"
+    h[other] = d[other] = None
+    g, _ = run(h, d, T, K, V, dtype)
+    less = m2rnn_ssm_bwd(*(d[n] for n in NAMES), d["H0"], d["dy"], dHT=d["dHT"], want_dh0=False)
+    assert less["dH0"] is None
+    assert all(torch.equal(g[n], less[n]) for n in g if n != "dH0")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,T,N,K,V", SPLITS + [(100, 70, 8, 40, 72)])
+def test_forward_without_the_last_state(B, T, N, K, V, dtype):
+    h, d = inputs(B, T, N, 1, K, V, dtype, seed=T + 1)
+    y, HT = m2rnn_ssm_fwd(*(d[n] for n in NAMES), H0=d["H0"], want_ht=False)
+    assert HT is None
+    assert torch.equal(y, m2rnn_ssm_fwd(*(d[n] for n in NAMES), H0=d["H0"])[0])
+    ry, _, _ = oracle.ssm_forward(*(h[n] for n in NAMES), h["H0"])
+    m, mH0 = magnitude(h)
+    Ay, _, _ = oracle.ssm_forward(*m, mH0)
+    check(y, ry, Ay, rel_bound(T, K, dtype, False), 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24, "y")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,T,N,NQ,K,V", [(2, 2000, 4, 4, 32, 128), (1, 1500, 8, 1, 64, 16), (2, 1100, 3, 3, 64, 64)])
+@pytest.mark.parametrize("carry", [True, False])
+def test_decays_gradients_by_their_norms(B, T, N, NQ, K, V, carry, dtype):
+    """The decays' gradients over many chunks and segments, closer than by the sums of absolute
+    values: roundings of 2^-24 in sums of some 300 terms add at random to 20 2^-24 = 1e-6 of the
+    terms, and terms of both signs leave at least a tenth of their norm: 1e-5."""
+    h, d = inputs(B, T, N, NQ, K, V, dtype, seed=T + V, carry=carry)
+    g = m2rnn_ssm_bwd(*(d[n] for n in NAMES), d["H0"], d["dy"], dHT=d["dHT"])
+    ref = oracle.ssm_backward(*(h[n] for n in NAMES), h["H0"], h["dy"], h["dHT"])
+    for n in ("dlogit", "dalpha", "dbeta"):
+        e = np.linalg.norm(g[n].cpu().double().numpy() - ref[n]) / np.linalg.norm(ref[n])
+        print(n, e)
+        assert e <= 1e-5, (n, e)
