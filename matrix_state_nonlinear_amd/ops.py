@@ -409,11 +409,12 @@ def _call(name, dev, *args):
             t = ctypes_ptr(t)
         vals.append(t)
     fn = getattr(_lib.lib(), name)
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*vals, _stream(dev))
+    index = dev.index
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*vals, torch._C._cuda_getCurrentRawStream(index))
     else:  # the launches go to the stream's own device
         with torch.cuda.device(dev):
-            st = fn(*vals, _stream(dev))
+            st = fn(*vals, torch._C._cuda_getCurrentRawStream(index))
     if st != _lib.M2RNN_OK:
         check(st, name)
 
@@ -533,8 +534,11 @@ def m2rnn_ssm_step(H, k, v, q, logit, alpha, beta, w_r, out=None):
     _need(alpha, (N,), f32, "alpha")
     _need(beta, (N,), f32, "beta")
     _need(w_r, (N, V), f32, "w_r")
-    y = torch.empty((B, N, V), dtype=v.dtype, device=H.device) if out is None else out
-    _need(y, (B, N, V), v.dtype, "out")
+    if out is None:
+        y = torch.empty_like(v)
+    else:
+        y = out
+        _need(y, (B, N, V), v.dtype, "out")
     _call("m2rnn_ssm_step", H.device, B, N, NQ, K, V, io, k, v, q, logit, alpha, beta, w_r, H, y)
     return y
 
@@ -603,8 +607,11 @@ def m2rnn_conv_step(hist, x, w, bias=None, out=None):
     _need(hist, (B, 3, C), x.dtype, "hist")
     _need(w, (C, 4), torch.float32, "w")
     _opt(bias, (C,), torch.float32, "bias")
-    o = torch.empty_like(x) if out is None else out
-    _need(o, (B, C), x.dtype, "out")
+    if out is None:
+        o = torch.empty_like(x)
+    else:
+        o = out
+        _need(o, (B, C), x.dtype, "out")
     _call("m2rnn_conv_step", x.device, B, C, io, x, w, bias, hist, o)
     return o
 
@@ -612,10 +619,11 @@ def m2rnn_conv_step(hist, x, w, bias=None, out=None):
 # ---- group norm with a gate
 
 def _groupnorm_sizes(y, g_pre, gamma, beta, groups):
-    D = y.shape[-1]
+    shape = y.shape
+    D = shape[-1]
     if groups < 1 or D < 1 or D % groups:
         raise ValueError(f"groups = {groups} must divide D = {D}")
-    _need(g_pre, tuple(y.shape), y.dtype, "g_pre")
+    _need(g_pre, shape, y.dtype, "g_pre")
     _need(gamma, (D,), torch.float32, "gamma")
     _need(beta, (D,), torch.float32, "beta")
     return y.numel() // D, D, _io_dtype(y, "y")
@@ -626,8 +634,11 @@ def m2rnn_groupnorm_gate(y, g_pre, gamma, beta, groups: int, eps: float = 1e-5, 
     ``groups`` runs of D / groups consecutive channels of the last dimension D.  y and g_pre
     [..., D] in float32 or bfloat16, gamma and beta [D] float32; returns [..., D] in y's dtype."""
     rows, D, io = _groupnorm_sizes(y, g_pre, gamma, beta, groups)
-    o = torch.empty_like(y) if out is None else out
-    _need(o, tuple(y.shape), y.dtype, "out")
+    if out is None:
+        o = torch.empty_like(y)
+    else:
+        o = out
+        _need(o, y.shape, y.dtype, "out")
     _call("m2rnn_groupnorm_gate", y.device, rows, D, int(groups), io, float(eps), y, g_pre, gamma,
           beta, o)
     return o
