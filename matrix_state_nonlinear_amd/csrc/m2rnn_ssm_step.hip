@@ -4,8 +4,9 @@
 // step is bound by HBM.  A wave (W = 1) or a workgroup of four takes a head: lanes run along V in
 // 16-byte pieces and then along K, four pieces per lane in flight; the columns' sums are
 // joined by lane exchanges and, for four waves, through LDS.  512 sequences of 16 heads, K = V = 64:
-// 46 us for 273 MB (5.9 TB/s, part of the state still in the memory-side cache from the step
-// before; 62 us after other work has emptied it, 4.4 TB/s); sixteen pieces in flight took 87.
+// 46.6 us for 273 MB (5.9 TB/s, part of the state still in the memory-side cache from the step
+// before); 58 us after other work has emptied it (4.7 TB/s; 63 with the state's loads behind the decay
+// instead of before it); sixteen pieces in flight took 87.
 #include "m2rnn_io.h"
 #include "m2rnn_ssm_internal.h"
 #include "m2rnn_ssm_sweep.h"
@@ -35,9 +36,26 @@ __global__ void __launch_bounds__(256) m2rnn_ssm_step_kernel(const SsmStepArgs g
   // lv lanes along V (a power of two), 64 / lv rows per pass of a wave
   const int lv = g.lanes_v, rows = 64 / lv;
   const int cl = lane & (lv - 1), r0 = wh * rows + lane / lv;
-  const float d = ssm::softplus(g.logit[unit] + g.beta[n]);
-  const float f = ssm::pow2(ssm::log2_decay(g.alpha[n], d));
-
+  // the first rows of the state are on their way while the decay is made
+  constexpr int U = 4;
+  const float logit = g.logit[unit], beta = g.beta[n], alpha = g.alpha[n];
+  io::Vals<VEC> h[U][NB];
+  float k[U], q[U];
+  auto load = [&](int r) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int row = r + i * rows * W;
+      const bool ok = row < K;
+      k[i] = ok ? load_in(kp + row) : 0.0f;
+      q[i] = ok ? load_in(qp + row) : 0.0f;
+#pragma unroll
+      for (int c = 0; c < NB; ++c) {
+        const int col = (c * lv + cl) * VEC;
+        if (ok && col < V) h[i][c] = io::load<VEC>(H + (int64_t)row * V + col);
+      }
+    }
+  };
+  load(r0);
   float v[NB][VEC], acc[NB][VEC];
 #pragma unroll
   for (int c = 0; c < NB; ++c)
@@ -47,22 +65,10 @@ __global__ void __launch_bounds__(256) m2rnn_ssm_step_kernel(const SsmStepArgs g
       v[c][j] = col < V ? load_in(vp + col) : 0.0f;
       acc[c][j] = 0.0f;
     }
-  constexpr int U = 4;
+  const float d = ssm::softplus(logit + beta);
+  const float f = ssm::pow2(ssm::log2_decay(alpha, d));
   for (int r = r0; r < K; r += rows * W * U) {
-    io::Vals<VEC> h[U][NB];
-    float kd[U], q[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int row = r + i * rows * W;
-      const bool ok = row < K;
-      kd[i] = ok ? load_in(kp + row) * d : 0.0f;
-      q[i] = ok ? load_in(qp + row) : 0.0f;
-#pragma unroll
-      for (int c = 0; c < NB; ++c) {
-        const int col = (c * lv + cl) * VEC;
-        if (ok && col < V) h[i][c] = io::load<VEC>(H + (int64_t)row * V + col);
-      }
-    }
+    if (r != r0) load(r);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int row = r + i * rows * W;
@@ -72,7 +78,7 @@ __global__ void __launch_bounds__(256) m2rnn_ssm_step_kernel(const SsmStepArgs g
         if (row < K && col < V) {
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
-            const float x = __builtin_fmaf(f, h[i][c].x[j], kd[i] * v[c][j]);
+            const float x = __builtin_fmaf(f, h[i][c].x[j], k[i] * d * v[c][j]);
             h[i][c].x[j] = x;
             acc[c][j] = __builtin_fmaf(x, q[i], acc[c][j]);
           }
@@ -135,11 +141,10 @@ hipError_t run(SsmStepArgs g, bool vec, hipStream_t stream) {
 
 hipError_t launch_ssm_step(const SsmStepArgs& g, int in_dtype, hipStream_t stream) {
   const bool vec = g.V % 4 == 0 && aligned16(g.H);
-  // a wave holds 4 x 64 x 4 elements in flight: larger heads are shared by four waves (8192 heads of
-  // 64 x 64: 45.8 us shared, 48.0 not; of 2048, 128 x 128: 45 and 60; but 32768 of 64 x 16: 84 and
-  // 48), and so are the heads of calls that would leave most CUs without a wave (64 of 64 x 16: 13.3 us
-  // and 14.1 with the call)
-  const bool split = g.K * g.V >= 4096 || (g.B * g.N < 512 && g.K * g.V >= 1024);
+  // a wave holds 4 x 64 x 4 elements in flight: larger heads are shared by four waves (2048 heads of
+  // 128 x 128: 43.8 us shared, 46.9 not; 8192 of 64 x 64: 46.6 both; 8192 of 32 x 64: 31.4 and 24.1; 32768
+  // of 64 x 16: 81 and 48)
+  const bool split = g.K * g.V >= 4096;
   if (in_dtype == kBF16)
     return split ? run<uint16_t, 4>(g, vec, stream) : run<uint16_t, 1>(g, vec, stream);
   return split ? run<float, 4>(g, vec, stream) : run<float, 1>(g, vec, stream);
